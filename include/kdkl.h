@@ -319,8 +319,135 @@ kdkl_status kdkl_teacher_topk(const void* hidden, const void* W, int64_t N, int3
                               void* stream);
 
 /*
- * Reads the device flag word of the most recent forward/backward call that
- * used `workspace` (each call clears it first).  Synchronises `stream`.
+ * ---------------------------------------------------------------------------
+ * Operators between a model's last layer and its output head, and back: the
+ * final RMS norm that produces `hidden`, and a linear layer for what may stand
+ * before it (a residual block of a draft head, a projection to the width of
+ * another model's head).  Their gradients take the loss's dHidden further back.
+ * Same conventions as above: dense row-major tensors of the current device,
+ * caller-owned workspaces, asynchronous on `stream`, host checks before any
+ * launch, results that repeat bit for bit; every call can be captured in a CUDA
+ * graph after one eager call.  Every row takes part: rows of padding hold finite
+ * values (a NaN or infinity in a row spreads to that row's outputs, and in a
+ * gradient to the column sums and weight gradients that the row enters).
+ * ---------------------------------------------------------------------------
+ */
+typedef enum { KDKL_BF16 = 0, KDKL_F32 = 1, KDKL_E4M3 = 2 } kdkl_dtype;
+
+/*
+ * RMS norm with the residual's addition:
+ *   h = x + residual            (h = x where residual is NULL), fp32
+ *   y = h / sqrt(mean_j h_j^2 + eps) * gamma
+ *   x           [N, d] of x_dtype (KDKL_BF16 or KDKL_F32), 16-byte aligned
+ *   residual    [N, d] of h_dtype (KDKL_BF16 or KDKL_F32), 16-byte aligned, or NULL
+ *   gamma       [d] of gamma_dtype (KDKL_BF16 or KDKL_F32), 16-byte aligned
+ *   h           [N, d] out of h_dtype, 16-byte aligned, or NULL: the sum, the next residual and what
+ *               kdkl_rmsnorm_backward reads.  y is computed from the sum before it is rounded to h_dtype.
+ *   y           [N, d] out, 16-byte aligned: KDKL_BF16 (the `hidden` of kdkl_forward), or KDKL_E4M3
+ *   y_scale     [N] fp32 out, 4-byte aligned, for KDKL_E4M3 only (else NULL): the row's largest |y| / 448;
+ *               the row's values are y_scale[n] * (e4m3 value).  A row of zeros has scale 0; a row with a
+ *               NaN has scale NaN.
+ *   N >= 0, d % 8 == 0, 8 <= d <= 32768, eps finite and >= 0
+ * h may be residual itself or, where the types agree, x; y may be x where both are bf16 and h is another
+ * buffer.  No workspace.  N = 0 writes nothing.
+ */
+kdkl_status kdkl_rmsnorm_forward(const void* x, const void* residual, const void* gamma, int64_t N, int32_t d,
+                                 float eps, int32_t x_dtype, int32_t h_dtype, int32_t gamma_dtype, int32_t y_dtype,
+                                 void* h, void* y, float* y_scale, void* stream);
+
+/*
+ * Gradient of the RMS norm at h (the statistics are recomputed from h), with xhat = h / sqrt(mean h^2 + eps):
+ *   dx     = (dy gamma - xhat mean_j(dy_j gamma_j xhat_j)) / sqrt(mean h^2 + eps) + dh
+ *   dgamma = sum_n dy[n] xhat[n]
+ *   dy      [N, d] bf16, 16-byte aligned (the dHidden of kdkl_backward)
+ *   h       [N, d] of h_dtype, 16-byte aligned;  gamma as in the forward
+ *   dh      [N, d] of h_dtype, 16-byte aligned, or NULL: the gradient that reaches h on its other way (the
+ *           residual stream)
+ *   dx      [N, d] out of h_dtype, 16-byte aligned: the gradient of x and of residual alike; may be dh
+ *   dgamma  [d] fp32 out, 4-byte aligned, overwritten
+ *   workspace >= kdkl_rmsnorm_workspace_bytes(N, d), 256-byte aligned (it holds no device flags)
+ * An e4m3 y has the same gradient: rounding is passed through.  N = 0 writes dgamma = 0.
+ */
+size_t kdkl_rmsnorm_workspace_bytes(int64_t N, int32_t d);
+kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gamma, const void* dh, int64_t N,
+                                  int32_t d, float eps, int32_t h_dtype, int32_t gamma_dtype, void* dx,
+                                  float* dgamma, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Linear layer with bias, activation and residual:
+ *   z = x W^T + bias,  y = act(z) + residual
+ *   x         [M, d_in], 16-byte aligned;  W [d_out, d_in], 16-byte aligned (nn.Linear layout)
+ *             KDKL_BF16: both bf16, d_in % 8 == 0
+ *             KDKL_E4M3: both e4m3 with fp32 scales, d_in % 16 == 0; x_scale [M] (4-byte aligned) and
+ *             w_scale [d_out] (16-byte aligned) multiply the product's rows and columns, so that an e4m3
+ *             y of kdkl_rmsnorm_forward and its y_scale can be passed as they are
+ *   bias      [d_out] bf16, 16-byte aligned, or NULL
+ *   residual  [M, d_out] bf16, 16-byte aligned, or NULL
+ *   y         [M, d_out] bf16 out, 16-byte aligned; may be residual itself
+ *   pre       [M, d_out] bf16 out, 16-byte aligned, or NULL: z for kdkl_linear_backward (act is applied to z
+ *             before it is rounded)
+ *   M >= 0, d_out % 8 == 0, d_in, d_out <= 2^20
+ *   options   NULL = bf16 operands, no activation, the planner's tiles
+ *   workspace >= kdkl_linear_workspace_bytes(M, d_in, d_out, 0), 256-byte aligned; it holds the device flag
+ *             word (kdkl_read_device_flags) and no other state.  Calls that may overlap need workspaces of
+ *             their own.
+ * Products are summed in fp32.  M = 0 writes nothing.
+ *
+ * Activations: KDKL_ACT_GELU is z Phi(z) (the error-function form), KDKL_ACT_GELU_TANH its tanh approximation,
+ * KDKL_ACT_SILU z / (1 + e^-z).
+ *
+ * Gradient, with dz = dy act'(pre) in bf16 (rounded once, as the operand of both products):
+ *   dx = dz W [M, d_in] bf16,  dW = dz^T x [d_out, d_in] bf16 (both summed in fp32 and rounded once),
+ *   dbias = sum_rows dy act'(pre) [d_out] fp32 (summed before the rounding of dz)
+ *   dy        [M, d_out] bf16, 16-byte aligned; it is also the gradient of residual
+ *   pre       [M, d_out] bf16, 16-byte aligned, as written by the forward; not read (and may be NULL) with
+ *             KDKL_ACT_NONE
+ *   dx, dW (16-byte aligned), dbias (4-byte aligned): any of them may be NULL, not all; overwritten.  x is
+ *             read for dW only and W for dx only; the other may be NULL.
+ *   workspace >= kdkl_linear_workspace_bytes(M, d_in, d_out, 1), 256-byte aligned
+ * KDKL_E4M3 operands have no gradient (KDKL_ERR_UNSUPPORTED).  M = 0 writes dW = 0 and dbias = 0.
+ */
+typedef enum {
+  KDKL_ACT_NONE = 0,
+  KDKL_ACT_RELU = 1,
+  KDKL_ACT_GELU = 2,
+  KDKL_ACT_GELU_TANH = 3,
+  KDKL_ACT_SILU = 4
+} kdkl_activation;
+
+typedef struct {
+  int32_t operands;      /* KDKL_BF16 (default) or KDKL_E4M3 */
+  int32_t activation;    /* kdkl_activation (default KDKL_ACT_NONE) */
+  const float* x_scale;  /* KDKL_E4M3: [M] fp32 */
+  const float* w_scale;  /* KDKL_E4M3: [d_out] fp32 */
+  /* Tiles of the products: 0 = the planner's choice (default), else a plan as kdkl_linear_plan reports it.
+   * 128, 192 or 256: tiles of 256 rows x that many columns, by CTA pairs.  1000 * splits + rows (splits 1, 2,
+   * 4 or 8, not above the 128-byte blocks of the reduction axis; rows 16, 32, 64 or 128): tiles of 128 columns
+   * x `rows` rows, the reduction split over a cluster of `splits` CTAs; not for dW. */
+  int32_t plan;          /* forward */
+  int32_t dx_plan;       /* gradient: dx */
+  int32_t dw_plan;       /* gradient: dW */
+} kdkl_linear_options;
+
+/* The products that kdkl_linear_plan plans. */
+typedef enum { KDKL_LINEAR_FORWARD = 0, KDKL_LINEAR_DX = 1, KDKL_LINEAR_DW = 2 } kdkl_linear_product;
+
+void kdkl_linear_options_init(kdkl_linear_options* options);
+size_t kdkl_linear_workspace_bytes(int64_t M, int32_t d_in, int32_t d_out, int32_t backward);
+/* Host only: the plan of a product on a device with `sm_count` SMs (0 = ask the current device). */
+kdkl_status kdkl_linear_plan(int64_t M, int32_t d_in, int32_t d_out, int32_t operands, int32_t product,
+                             int32_t sm_count, int32_t* plan_out);
+kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, const void* residual, int64_t M,
+                                int32_t d_in, int32_t d_out, const kdkl_linear_options* options, void* y, void* pre,
+                                void* workspace, size_t workspace_bytes, void* stream);
+kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x, const void* W, int64_t M,
+                                 int32_t d_in, int32_t d_out, const kdkl_linear_options* options, void* dx, void* dW,
+                                 float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Reads the device flag word of the most recent forward/backward call (of the
+ * loss, the top-K producer or the linear layer) that used `workspace` (each call
+ * clears it first).  Synchronises `stream`.
  */
 kdkl_status kdkl_read_device_flags(const void* workspace, void* stream, uint32_t* flags_out);
 
@@ -335,7 +462,8 @@ kdkl_status kdkl_read_device_flags(const void* workspace, void* stream, uint32_t
  */
 typedef struct {
   const char* name;   /* "prepass", "fwd_lse_gemm", "merge", "bwd_grad_gemm", "bwd_dhidden_gemm", "bwd_dw_gemm",
-                         "teacher_topk_gemm", "teacher_topk_merge" */
+                         "teacher_topk_gemm", "teacher_topk_merge", "fused_fwd_gemm", "fused_g_pass", "rmsnorm",
+                         "rmsnorm_grad", "linear_gemm", "linear_act_grad", "linear_dx_gemm", "linear_dw_gemm" */
   uint64_t launches;  /* launches timed since the last reset */
   double total_ms;    /* summed device time of those launches */
 } kdkl_kernel_time;

@@ -8,6 +8,8 @@ raises.
 Names mirror the C entry points: ``kdkl_workspace_bytes``, ``kdkl_forward``,
 ``kdkl_backward``, ``kdkl_forward_ex``, ``kdkl_backward_ex`` (with ``kdkl_options``),
 ``kdkl_forward_noalloc``, ``kdkl_teacher_topk``, ``kdkl_count_valid``, ``kdkl_read_device_flags``, ``kdkl_timing_enable``,
+``kdkl_rmsnorm_forward``, ``kdkl_rmsnorm_backward``, ``kdkl_linear_forward``, ``kdkl_linear_backward``,
+``kdkl_linear_plan`` (the operators ahead of the head),
 ``kdkl_timing_read``, ``kdkl_status_string``, ``kdkl_last_error``; with the profiling build loaded,
 ``kdkl_profile_role_cycles_read`` / ``kdkl_profile_role_cycles_clear`` (``include/kdkl_profile.h``).
 ``fused_kl_forward_backward`` is a convenience wrapper
@@ -30,6 +32,12 @@ KDKL_OK = 0
 STATUS_NAMES = {0: "KDKL_OK", 1: "KDKL_ERR_NULL", 2: "KDKL_ERR_SHAPE", 3: "KDKL_ERR_ALIGN",
                 4: "KDKL_ERR_UNSUPPORTED", 5: "KDKL_ERR_WORKSPACE", 6: "KDKL_ERR_CUDA"}
 DEV_IDX_RANGE, DEV_IDX_DUP, DEV_NONFINITE, DEV_TIMEOUT, DEV_BOUNDS = 1, 2, 4, 8, 16
+
+# kdkl_dtype, kdkl_activation and kdkl_linear_product
+BF16, F32, E4M3 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
+LINEAR_FORWARD, LINEAR_DX, LINEAR_DW = 0, 1, 2
 
 _lib = None
 
@@ -63,6 +71,13 @@ def kdkl_options(cache_format=CACHE_I32_F32, student_tau=1.0, kd_weight=1.0, kd_
     # the struct holds raw device addresses: keep the tensors alive as long as it lives
     o._keep = (labels, n_valid_global)
     return o
+
+
+class LinearOptions(ctypes.Structure):
+    """kdkl_linear_options (see include/kdkl.h)."""
+    _fields_ = [("operands", ctypes.c_int32), ("activation", ctypes.c_int32), ("x_scale", ctypes.c_void_p),
+                ("w_scale", ctypes.c_void_p), ("plan", ctypes.c_int32), ("dx_plan", ctypes.c_int32),
+                ("dw_plan", ctypes.c_int32)]
 
 
 class KDKLError(RuntimeError):
@@ -123,6 +138,23 @@ def lib() -> ctypes.CDLL:
     L.kdkl_backward_plan.argtypes = [i64, i32, i32, i32, i64, ctypes.POINTER(Options), i32,
                                      ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)]
     L.kdkl_backward_plan.restype = ctypes.c_int
+    L.kdkl_rmsnorm_forward.argtypes = [vp, vp, vp, i64, i32, f32, i32, i32, i32, i32, vp, vp, vp, vp]
+    L.kdkl_rmsnorm_forward.restype = ctypes.c_int
+    L.kdkl_rmsnorm_workspace_bytes.argtypes = [i64, i32]
+    L.kdkl_rmsnorm_workspace_bytes.restype = sz
+    L.kdkl_rmsnorm_backward.argtypes = [vp, vp, vp, vp, i64, i32, f32, i32, i32, vp, vp, vp, sz, vp]
+    L.kdkl_rmsnorm_backward.restype = ctypes.c_int
+    L.kdkl_linear_options_init.argtypes = [ctypes.POINTER(LinearOptions)]
+    L.kdkl_linear_options_init.restype = None
+    L.kdkl_linear_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    L.kdkl_linear_workspace_bytes.restype = sz
+    L.kdkl_linear_plan.argtypes = [i64, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_int32)]
+    L.kdkl_linear_plan.restype = ctypes.c_int
+    L.kdkl_linear_forward.argtypes = [vp, vp, vp, vp, i64, i32, i32, ctypes.POINTER(LinearOptions), vp, vp, vp, sz, vp]
+    L.kdkl_linear_forward.restype = ctypes.c_int
+    L.kdkl_linear_backward.argtypes = [vp, vp, vp, vp, i64, i32, i32, ctypes.POINTER(LinearOptions), vp, vp, vp, vp,
+                                       sz, vp]
+    L.kdkl_linear_backward.restype = ctypes.c_int
     if hasattr(L, "kdkl_profile_read_role_cycles"):
         L.kdkl_profile_role_cycles_shape.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
         L.kdkl_profile_role_cycles_shape.restype = ctypes.c_int
@@ -335,6 +367,162 @@ def kdkl_count_valid(topk_idx, topk_logit, mask, tau, V, workspace, options=None
                                 opt, _ptr(workspace), int(wsb), _stream(stream))
     if check:
         _check(st, "kdkl_count_valid")
+    return st
+
+
+# ---------------------------------------------------------------- operators ahead of the head
+def _bad(status: int, where: str, detail: str):
+    raise KDKLError(status, where, detail)
+
+
+def _tensor(where, name, t, shape, dtypes, device) -> int | None:
+    """Address of a tensor argument after checking its shape, type, layout and device (None stays None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        _bad(2, where, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        _bad(4, where, f"{name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if not t.is_contiguous():
+        _bad(2, where, f"{name} must be dense row-major")
+    if t.device != device:
+        _bad(4, where, f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _where(where, t, name):
+    """The current device, after checking that `t`, a CUDA tensor of two dimensions, is on it."""
+    import torch
+    if t.dim() != 2:
+        _bad(2, where, f"{name} has {t.dim()} dimensions, expected 2")
+    dev = t.device
+    if dev.type != "cuda":
+        _bad(4, where, f"{name} is on {dev}, expected the current CUDA device")
+    if dev.index != torch.cuda.current_device():
+        _bad(4, where, f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch, dev
+
+
+def _workspace(where, ws, device):
+    if ws.device != device:
+        _bad(4, where, f"workspace is on {ws.device}, expected {device}")
+    if not ws.is_contiguous():
+        _bad(2, where, "workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def kdkl_rmsnorm_forward(x, gamma, y, *, residual=None, h=None, y_scale=None, eps=1e-6, stream=None,
+                         check=True) -> int:
+    """Calls kdkl_rmsnorm_forward: h = x + residual, y = h / sqrt(mean h^2 + eps) * gamma.
+
+    x [N, d] and residual / h (of one type, bf16 or fp32), gamma [d]; y bf16, or float8_e4m3fn with y_scale [N].
+    """
+    fn = "kdkl_rmsnorm_forward"
+    torch, dev = _where(fn, x, "x")
+    bf, f32 = torch.bfloat16, torch.float32
+    N, d = shape = x.shape
+    hd = residual.dtype if residual is not None else (h.dtype if h is not None else x.dtype)
+    fl = (bf, f32)
+    st = lib().kdkl_rmsnorm_forward(
+        _tensor(fn, "x", x, shape, fl, dev), _tensor(fn, "residual", residual, shape, fl, dev),
+        _tensor(fn, "gamma", gamma, (d,), fl, dev), N, d, eps, F32 if x.dtype == f32 else BF16,
+        F32 if hd == f32 else BF16, F32 if gamma.dtype == f32 else BF16, BF16 if y.dtype == bf else E4M3,
+        _tensor(fn, "h", h, shape, (hd,), dev), _tensor(fn, "y", y, shape, (bf, torch.float8_e4m3fn), dev),
+        _tensor(fn, "y_scale", y_scale, (N,), (f32,), dev), _stream(stream))
+    if check:
+        _check(st, fn)
+    return st
+
+
+def kdkl_rmsnorm_workspace_bytes(N: int, d: int) -> int:
+    return int(lib().kdkl_rmsnorm_workspace_bytes(N, d))
+
+
+def kdkl_rmsnorm_backward(dy, h, gamma, dx, dgamma, workspace, *, dh=None, eps=1e-6, stream=None, check=True) -> int:
+    """Calls kdkl_rmsnorm_backward: dx (the gradient of x and residual alike, plus dh) and dgamma."""
+    fn = "kdkl_rmsnorm_backward"
+    torch, dev = _where(fn, h, "h")
+    bf, f32 = torch.bfloat16, torch.float32
+    N, d = shape = h.shape
+    hd = (h.dtype,)
+    ws, wsb = _workspace(fn, workspace, dev)
+    st = lib().kdkl_rmsnorm_backward(
+        _tensor(fn, "dy", dy, shape, (bf,), dev), _tensor(fn, "h", h, shape, (bf, f32), dev),
+        _tensor(fn, "gamma", gamma, (d,), (bf, f32), dev), _tensor(fn, "dh", dh, shape, hd, dev), N, d, eps,
+        F32 if h.dtype == f32 else BF16, F32 if gamma.dtype == f32 else BF16, _tensor(fn, "dx", dx, shape, hd, dev),
+        _tensor(fn, "dgamma", dgamma, (d,), (f32,), dev), ws, wsb, _stream(stream))
+    if check:
+        _check(st, fn)
+    return st
+
+
+def _activation(where, a) -> int:
+    if isinstance(a, str):
+        if a not in ACTIVATIONS:
+            _bad(4, where, f"unknown activation {a!r}")
+        return ACTIVATIONS[a]
+    return int(a)
+
+
+def kdkl_linear_workspace_bytes(M: int, d_in: int, d_out: int, backward: bool = False) -> int:
+    return int(lib().kdkl_linear_workspace_bytes(M, d_in, d_out, 1 if backward else 0))
+
+
+def kdkl_linear_plan(M: int, d_in: int, d_out: int, operands: int = BF16, product: int = LINEAR_FORWARD,
+                     sm_count: int = 0) -> int:
+    """The tiles (a plan code, see include/kdkl.h) of one of the linear layer's products."""
+    out = ctypes.c_int32()
+    _check(lib().kdkl_linear_plan(int(M), int(d_in), int(d_out), int(operands), int(product), int(sm_count),
+                                  ctypes.byref(out)), "kdkl_linear_plan")
+    return out.value
+
+
+def kdkl_linear_forward(x, W, y, workspace, *, bias=None, residual=None, pre=None, activation="none", x_scale=None,
+                        w_scale=None, plan=0, stream=None, check=True) -> int:
+    """Calls kdkl_linear_forward: y = act(x W^T + bias) + residual; pre receives z = x W^T + bias.
+
+    x [M, d_in] and W [d_out, d_in] both bf16, or both float8_e4m3fn with x_scale [M] and w_scale [d_out].
+    """
+    fn = "kdkl_linear_forward"
+    torch, dev = _where(fn, x, "x")
+    bf, f32 = (torch.bfloat16,), (torch.float32,)
+    M, d_in = x.shape
+    d_out = W.shape[0]
+    out = (M, d_out)
+    ws, wsb = _workspace(fn, workspace, dev)
+    o = LinearOptions(E4M3 if x.dtype == torch.float8_e4m3fn else BF16, _activation(fn, activation),
+                      _tensor(fn, "x_scale", x_scale, (M,), f32, dev),
+                      _tensor(fn, "w_scale", w_scale, (d_out,), f32, dev), plan, 0, 0)
+    st = lib().kdkl_linear_forward(
+        _tensor(fn, "x", x, x.shape, (torch.bfloat16, torch.float8_e4m3fn), dev),
+        _tensor(fn, "W", W, (d_out, d_in), (x.dtype,), dev), _tensor(fn, "bias", bias, (d_out,), bf, dev),
+        _tensor(fn, "residual", residual, out, bf, dev), M, d_in, d_out, ctypes.byref(o),
+        _tensor(fn, "y", y, out, bf, dev), _tensor(fn, "pre", pre, out, bf, dev), ws, wsb, _stream(stream))
+    if check:
+        _check(st, fn)
+    return st
+
+
+def kdkl_linear_backward(dy, x, W, dx, dW, workspace, *, pre=None, dbias=None, activation="none", dx_plan=0,
+                         dw_plan=0, stream=None, check=True) -> int:
+    """Calls kdkl_linear_backward: dx = dz W, dW = dz^T x, dbias = sum dz with dz = dy act'(pre).
+
+    dx, dW and dbias may each be None; the gradient of the forward's residual is dy itself.
+    """
+    fn = "kdkl_linear_backward"
+    torch, dev = _where(fn, dy, "dy")
+    bf = (torch.bfloat16,)
+    M, d_out = out = dy.shape
+    d_in = W.shape[-1] if W is not None else (x.shape[-1] if x is not None else 8)   # 8: neither is read
+    ws, wsb = _workspace(fn, workspace, dev)
+    o = LinearOptions(BF16, _activation(fn, activation), None, None, 0, dx_plan, dw_plan)
+    st = lib().kdkl_linear_backward(
+        _tensor(fn, "dy", dy, out, bf, dev), _tensor(fn, "pre", pre, out, bf, dev),
+        _tensor(fn, "x", x, (M, d_in), bf, dev), _tensor(fn, "W", W, (d_out, d_in), bf, dev), M, d_in, d_out,
+        ctypes.byref(o), _tensor(fn, "dx", dx, (M, d_in), bf, dev), _tensor(fn, "dW", dW, (d_out, d_in), bf, dev),
+        _tensor(fn, "dbias", dbias, (d_out,), (torch.float32,), dev), ws, wsb, _stream(stream))
+    if check:
+        _check(st, fn)
     return st
 
 

@@ -28,7 +28,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libkdkl.so")
 DEBUG_LIB = os.path.join(OUT_DIR, "libkdkl_debug.so")
 PROFILE_LIB = os.path.join(OUT_DIR, "libkdkl_prof.so")
-SOURCES = ("kernels.cu", "api.cu", "noalloc.cu")
+SOURCES = ("kernels.cu", "api.cu", "noalloc.cu", "norm.cu", "linear.cu", "layer_api.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

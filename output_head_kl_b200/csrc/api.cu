@@ -19,12 +19,15 @@
 #include <vector>
 
 #include "../../include/kdkl.h"
+#include "host_util.h"
 #include "kdkl_internal.h"
 
 namespace kdkl {
 namespace {
 
 thread_local char g_last_error[256] = {0};
+
+}  // namespace
 
 kdkl_status fail(kdkl_status st, const char* fmt, ...) {
   va_list ap;
@@ -39,9 +42,7 @@ kdkl_status ok() {
   return KDKL_OK;
 }
 
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 constexpr int64_t kDefaultChunk = 8192;
 constexpr int kDefaultSyncWindow = 1;      // row-stream GEMMs: tiles (measured best of 0, 1, 2, 4, 8)
@@ -49,7 +50,6 @@ constexpr int kDefaultSyncKWindow = 64;    // tile-mode GEMMs: reduction blocks 
 constexpr int kSplitGroupMB = 32;          // split-major GEMMs: hidden rows per row-block group
 constexpr int kTileColGroup = 0;           // dHidden / dW: column tiles per group (0 = all)
 constexpr int kDieOrder = 0;               // GEMM groups numbered by block index
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256;
 constexpr int32_t kMaxV = (int32_t(1) << 30);
 
 // --------------------------------------------------------------- tensor maps
@@ -71,6 +71,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // 2-D bf16 map: `inner` contiguous elements per row, `outer` rows, row pitch in elements.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_elems,
               uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
@@ -84,6 +86,22 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, 
             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// The same for a matrix of bytes (8-bit elements).
+bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_elems,
+                 uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {pitch_elems};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
 
 // The same for an fp32 matrix.
 bool make_map_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_elems,
@@ -99,13 +117,9 @@ bool make_map_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t out
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// --------------------------------------------------------------- planner
-struct Device {
-  int id = 0;
-  int sms = 0;
-  int cc_major = 0;
-};
+}  // namespace
 
+// --------------------------------------------------------------- planner
 kdkl_status current_device(Device& dv) {
   if (cudaGetDevice(&dv.id) != cudaSuccess) return fail(KDKL_ERR_UNSUPPORTED, "no CUDA device is current");
   if (cudaDeviceGetAttribute(&dv.sms, cudaDevAttrMultiProcessorCount, dv.id) != cudaSuccess ||
@@ -122,6 +136,8 @@ int env_window(const char* name, int dflt) {
   if (e && *e) v = std::atoi(e);
   return v < 0 ? 0 : v;
 }
+
+namespace {
 
 // Vocabulary splits for a row-stream kernel over `rb` row blocks and `vt`
 // vocabulary tiles: balance the per-group tile count over `ctas` CTA groups
@@ -384,17 +400,20 @@ T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
 }
 
+}  // namespace
+
 kdkl_status cuda_fail(cudaError_t e, const char* what) {
   return fail(KDKL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+namespace {
+
 // ---------------------------------------------------------------- timing
-enum TimedKind {
-  kTPrepass = 0, kTFwd, kTMerge, kTGrad, kTDh, kTDw, kTTopK, kTTopKMerge, kTFusedFwd, kTGPass, kTKinds
-};
 const char* const kTimedNames[kTKinds] = {"prepass",          "fwd_lse_gemm", "merge",         "bwd_grad_gemm",
                                           "bwd_dhidden_gemm", "bwd_dw_gemm",  "teacher_topk_gemm",
-                                          "teacher_topk_merge", "fused_fwd_gemm", "fused_g_pass"};
+                                          "teacher_topk_merge", "fused_fwd_gemm", "fused_g_pass",
+                                          "rmsnorm", "rmsnorm_grad", "linear_gemm", "linear_act_grad",
+                                          "linear_dx_gemm", "linear_dw_gemm"};
 struct TimingRec {
   int kind;
   cudaEvent_t a, b;
@@ -405,23 +424,19 @@ std::vector<TimingRec> g_pending;
 uint64_t g_launches[kTKinds] = {0};
 double g_ms[kTKinds] = {0};
 
-template <class F>
-cudaError_t timed(int kind, cudaStream_t s, F&& launch) {
-  bool on;
-  {
-    std::lock_guard<std::mutex> lk(g_tmu);
-    on = g_timing;
-  }
-  if (!on) return launch();
-  cudaEvent_t a = nullptr, b = nullptr;
-  if (cudaEventCreate(&a) != cudaSuccess || cudaEventCreate(&b) != cudaSuccess) return cudaGetLastError();
-  cudaEventRecord(a, s);
-  const cudaError_t e = launch();
-  cudaEventRecord(b, s);
+}  // namespace
+
+bool timing_on() {
+  std::lock_guard<std::mutex> lk(g_tmu);
+  return g_timing;
+}
+
+void timing_add(int kind, cudaEvent_t a, cudaEvent_t b) {
   std::lock_guard<std::mutex> lk(g_tmu);
   g_pending.push_back({kind, a, b});
-  return e;
 }
+
+namespace {
 
 // Prepass shared by forward and backward (the backward keeps no state from the forward).
 kdkl_status run_prepass(const Common& c, const WsLayout& L, cudaStream_t s) {

@@ -1,0 +1,473 @@
+// C ABI of the operators ahead of the output head (RMS norm, linear layer): argument checks, tile
+// planner, TMA descriptors and launches.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "../../include/kdkl.h"
+#include "host_util.h"
+#include "kdkl_internal.h"
+#include "layer_internal.h"
+
+namespace kdkl {
+namespace {
+
+constexpr int32_t kMaxWidth = 1 << 20;
+constexpr size_t kFlagBytes = 256;
+
+bool float_dtype(int32_t t) { return t == KDKL_BF16 || t == KDKL_F32; }
+
+// ---------------------------------------------------------------- RMS norm
+kdkl_status check_norm(int64_t N, int32_t d, float eps, int32_t h_dtype, int32_t gamma_dtype) {
+  if (N < 0 || N > kMaxRows) return fail(KDKL_ERR_SHAPE, "N=%lld outside [0, %lld]", (long long)N, (long long)kMaxRows);
+  if (d < 8 || d % 8 != 0) return fail(KDKL_ERR_SHAPE, "d=%d must be a positive multiple of 8", d);
+  if (d > kNormMaxD) return fail(KDKL_ERR_UNSUPPORTED, "d=%d above %d", d, kNormMaxD);
+  if (!std::isfinite(eps) || eps < 0.f) return fail(KDKL_ERR_SHAPE, "eps must be finite and >= 0");
+  if (!float_dtype(h_dtype) || !float_dtype(gamma_dtype))
+    return fail(KDKL_ERR_UNSUPPORTED, "h and gamma must be KDKL_BF16 or KDKL_F32");
+  return KDKL_OK;
+}
+
+size_t norm_part_bytes(int64_t N, int32_t d) {
+  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(N, kNormGradBlocks));
+  return align_up(static_cast<size_t>(rows) * d * 4, 256);
+}
+
+// ---------------------------------------------------------------- linear layer
+struct Plan {
+  bool pair = true;
+  int tile = 256;    // pair: columns of a tile; small: rows of a tile
+  int splits = 1;
+  int code() const { return pair ? tile : splits * 1000 + tile; }
+};
+
+// Product out[rows, cols] with `k_blocks` reduction blocks.
+//
+// Cost model in SM cycles.  Pair tiles: waves of ceil(tiles / pairs) tiles, each k_blocks x (2 x BN)
+// cycles of MMA at the tile's measured efficiency, then the last epilogue.  Small tiles: the larger of the
+// operand bytes that the SMs and the memory can move and one CTA's own chain of loads, plus the join.
+// Whichever is cheaper runs; the constants come from timing every plan over M = 1 to 4096 (the table in
+// front of plan_linear).
+Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
+  Plan best;
+  double lo = 1e300;
+  const int pairs = sms / 2;
+  const int64_t rb = (rows + 255) / 256;
+  for (int bn : {256, 192, 128}) {
+    const int64_t tiles = rb * ((cols + bn - 1) / bn);
+    const int64_t waves = (tiles + pairs - 1) / pairs;
+    const double eff = bn == 256 ? 0.85 : (bn == 192 ? 0.78 : 0.68);
+    const double c = static_cast<double>(waves) * (k_blocks * 2.0 * bn / eff + 700.0) + 6000.0;
+    if (c < lo * 0.99) {
+      lo = c;
+      best.pair = true;
+      best.tile = bn;
+      best.splits = 1;
+    }
+  }
+  if (op == kLinDw) return best;
+  for (int nt : {16, 32, 64, 128}) {
+    const int64_t tiles = ((cols + 127) / 128) * ((rows + nt - 1) / nt);
+    for (int sp : {1, 2, 4, 8}) {
+      if (sp > k_blocks) break;
+      const int64_t ctas = tiles * sp;
+      if (ctas > INT_MAX / 2) break;
+      const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
+      const double kb = std::ceil(static_cast<double>(k_blocks) / sp);
+      const double share = ctas > sms ? 2.0 : 1.0;                  // CTAs on the busiest SM
+      const double per_kb = (16384.0 + 128.0 * nt) / 48.0 * share;  // bytes one SM streams per cycle
+      const double c = waves * (kb * per_kb + 1200.0 * share) + 5000.0 + 350.0 * sp;
+      if (c < lo * 0.99) {
+        lo = c;
+        best.pair = false;
+        best.tile = nt;
+        best.splits = sp;
+      }
+    }
+  }
+  return best;
+}
+
+// A plan code of the caller's; false when the product has no such plan.
+bool decode_plan(int32_t code, LinOp op, int k_blocks, Plan& p) {
+  if (code == 128 || code == 192 || code == 256) {
+    p = Plan{true, code, 1};
+    return true;
+  }
+  if (op == kLinDw || code < 1000) return false;
+  const int sp = code / 1000, nt = code % 1000;
+  if (sp != 1 && sp != 2 && sp != 4 && sp != 8) return false;
+  if (nt != 16 && nt != 32 && nt != 64 && nt != 128) return false;
+  if (sp > k_blocks) return false;
+  p = Plan{false, nt, sp};
+  return true;
+}
+
+kdkl_status check_linear_shape(int64_t M, int32_t d_in, int32_t d_out, int32_t operands) {
+  if (operands != KDKL_BF16 && operands != KDKL_E4M3)
+    return fail(KDKL_ERR_UNSUPPORTED, "operands must be KDKL_BF16 or KDKL_E4M3");
+  if (M < 0 || M > kMaxRows) return fail(KDKL_ERR_SHAPE, "M=%lld outside [0, %lld]", (long long)M, (long long)kMaxRows);
+  const int step = operands == KDKL_E4M3 ? 16 : 8;
+  if (d_in < step || d_in % step != 0) return fail(KDKL_ERR_SHAPE, "d_in=%d must be a positive multiple of %d", d_in, step);
+  if (d_out < 8 || d_out % 8 != 0) return fail(KDKL_ERR_SHAPE, "d_out=%d must be a positive multiple of 8", d_out);
+  if (d_in > kMaxWidth || d_out > kMaxWidth) return fail(KDKL_ERR_UNSUPPORTED, "d_in=%d, d_out=%d above %d", d_in, d_out, kMaxWidth);
+  // output tiles are counted in 32 bits (the smallest tiles: 16 rows x 128 columns, up to 8 CTAs each,
+  // are only planned within it); the large tiles set the limit
+  const int64_t rb = (M + 255) / 256;
+  if (rb * ((std::max(d_in, d_out) + 127) / 128) > INT_MAX / 2)
+    return fail(KDKL_ERR_UNSUPPORTED, "M=%lld with d_in=%d, d_out=%d has too many output tiles", (long long)M, d_in, d_out);
+  return KDKL_OK;
+}
+
+kdkl_linear_options default_linear_options() {
+  kdkl_linear_options o;
+  std::memset(&o, 0, sizeof(o));
+  o.operands = KDKL_BF16;
+  o.activation = KDKL_ACT_NONE;
+  return o;
+}
+
+struct LinearLayout {
+  size_t dz = 0, part = 0, total = 0;
+};
+
+// Gradient workspace: the flag word, dz, and the partial column sums of the most blocks act_grad runs.
+LinearLayout linear_layout(int64_t M, int32_t d_out, bool backward) {
+  LinearLayout L;
+  size_t off = kFlagBytes;
+  if (backward) {
+    L.dz = off;
+    off = align_up(off + static_cast<size_t>(M) * d_out * 2, 256);
+    L.part = off;
+    off = align_up(off + static_cast<size_t>(act_grad_chunks(M, d_out, kMaxSms)) * d_out * 4, 256);
+  }
+  L.total = off;
+  return L;
+}
+
+int reduction_blocks(int32_t len, bool f8) { return (len + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
+
+// One product: out[rows, cols] (bf16) of `op`'s operands a [rows or reduction] and b.
+//   kLinFwd(E4M3): a = x [rows, len], b = W [cols, len]
+//   kLinDx:        a = dz [rows, len], b = W [len, cols]
+//   kLinDw:        a = dz [len, rows], b = x [len, cols]
+cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b, int64_t rows, int64_t cols,
+                        int64_t len, LinParams p, int sms, cudaStream_t s) {
+  const bool f8 = op == kLinFwdE4M3;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  p.M = static_cast<int>(rows);
+  p.N = static_cast<int>(cols);
+  p.k_blocks = reduction_blocks(static_cast<int32_t>(len), f8);
+  p.splits = plan.splits;
+  CUtensorMap tmA, tmB;
+  bool made;
+  if (plan.pair) {
+    const int bn = plan.tile;
+    if (f8)
+      made = make_map_u8(&tmA, a, len, rows, len, 128, kBM, sw) && make_map_u8(&tmB, b, len, cols, len, 128, bn / 2, sw);
+    else if (op == kLinFwd)
+      made = make_map(&tmA, a, len, rows, len, 64, kBM, sw) && make_map(&tmB, b, len, cols, len, 64, bn / 2, sw);
+    else if (op == kLinDx)
+      made = make_map(&tmA, a, len, rows, len, 64, kBM, sw) && make_map(&tmB, b, cols, len, cols, 64, 64, sw);
+    else
+      made = make_map(&tmA, a, rows, len, rows, 64, 64, sw) && make_map(&tmB, b, cols, len, cols, 64, 64, sw);
+    CUtensorMap tmOut, tmPre;
+    made = made && make_map(&tmOut, p.out, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+           make_map(&tmPre, p.pre ? p.pre : p.out, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!made) return cudaErrorInvalidValue;
+    p.n_tiles = static_cast<int>((cols + bn - 1) / bn);
+    p.units = static_cast<int>((rows + 255) / 256) * p.n_tiles;
+    p.row_group = 8;
+    const int groups = std::min(p.units, sms / 2);
+    return launch_linear_pair(op, bn, tmA, tmB, tmOut, tmPre, p, 2 * groups, s);
+  }
+  // small tiles: the weights take the MMA's M side
+  const int nt = plan.tile;
+  if (f8)
+    made = make_map_u8(&tmA, b, len, cols, len, 128, 128, sw) && make_map_u8(&tmB, a, len, rows, len, 128, nt, sw);
+  else if (op == kLinFwd)
+    made = make_map(&tmA, b, len, cols, len, 64, 128, sw) && make_map(&tmB, a, len, rows, len, 64, nt, sw);
+  else
+    made = make_map(&tmA, b, cols, len, cols, 64, 64, sw) && make_map(&tmB, a, len, rows, len, 64, nt, sw);
+  if (!made) return cudaErrorInvalidValue;
+  return launch_linear_small(op, nt, tmA, tmB, p, s);
+}
+
+kdkl_status pick_plan(int32_t code, LinOp op, int64_t rows, int64_t cols, int64_t len, int sms, const char* name,
+                      Plan& plan) {
+  const int kb = reduction_blocks(static_cast<int32_t>(std::min<int64_t>(len, INT_MAX / 2)), op == kLinFwdE4M3);
+  if (code == 0) {
+    plan = plan_linear(op, rows, cols, kb, sms);
+    return KDKL_OK;
+  }
+  if (!decode_plan(code, op, kb, plan)) return fail(KDKL_ERR_UNSUPPORTED, "%s=%d is no plan of this product", name, code);
+  const int64_t tiles = plan.pair ? 0 : ((cols + 127) / 128) * ((rows + plan.tile - 1) / plan.tile) * plan.splits;
+  if (tiles > INT_MAX / 2) return fail(KDKL_ERR_UNSUPPORTED, "%s=%d has too many tiles", name, code);
+  return KDKL_OK;
+}
+
+kdkl_status check_activation(int32_t act) {
+  if (act < KDKL_ACT_NONE || act > KDKL_ACT_SILU) return fail(KDKL_ERR_UNSUPPORTED, "unknown activation %d", act);
+  return KDKL_OK;
+}
+
+kdkl_status device_with_pairs(Device& dv) {
+  const kdkl_status st = current_device(dv);
+  if (st != KDKL_OK) return st;
+  if (dv.sms < 2) return fail(KDKL_ERR_UNSUPPORTED, "the linear layer needs CTA pairs");
+  return KDKL_OK;
+}
+
+// In the bounds-checking build the kernels' checks can fail at once, so the flag word is cleared ahead of
+// the launch; in the normal build the call's first kernel clears it (linear.cu, clear_flags).
+kdkl_status debug_clear(void* workspace, cudaStream_t s) {
+#ifdef KDKL_DEBUG
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+#else
+  (void)workspace;
+  (void)s;
+#endif
+  return KDKL_OK;
+}
+
+}  // namespace
+}  // namespace kdkl
+
+using namespace kdkl;
+
+extern "C" {
+
+kdkl_status kdkl_rmsnorm_forward(const void* x, const void* residual, const void* gamma, int64_t N, int32_t d,
+                                 float eps, int32_t x_dtype, int32_t h_dtype, int32_t gamma_dtype, int32_t y_dtype,
+                                 void* h, void* y, float* y_scale, void* stream) {
+  kdkl_status st = check_norm(N, d, eps, h_dtype, gamma_dtype);
+  if (st != KDKL_OK) return st;
+  if (!float_dtype(x_dtype)) return fail(KDKL_ERR_UNSUPPORTED, "x must be KDKL_BF16 or KDKL_F32");
+  if (y_dtype != KDKL_BF16 && y_dtype != KDKL_E4M3) return fail(KDKL_ERR_UNSUPPORTED, "y must be KDKL_BF16 or KDKL_E4M3");
+  if (!x || !gamma || !y) return fail(KDKL_ERR_NULL, "x, gamma and y must be non-NULL");
+  if ((y_dtype == KDKL_E4M3) != (y_scale != nullptr))
+    return fail(KDKL_ERR_NULL, "y_scale goes with a KDKL_E4M3 y, and only with one");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(h, 16) || !aligned(y, 16))
+    return fail(KDKL_ERR_ALIGN, "x, residual, gamma, h and y must be 16-byte aligned");
+  if (!aligned(y_scale, 4)) return fail(KDKL_ERR_ALIGN, "y_scale must be 4-byte aligned");
+  Device dv;
+  if ((st = current_device(dv)) != KDKL_OK) return st;
+  if (N == 0) return ok();
+  NormParams p;
+  p.x = x;
+  p.residual = residual;
+  p.gamma = gamma;
+  p.h = h;
+  p.y = y;
+  p.y_scale = y_scale;
+  p.N = N;
+  p.d = d;
+  p.eps = eps;
+  p.x_f32 = x_dtype == KDKL_F32;
+  p.h_f32 = h_dtype == KDKL_F32;
+  p.gamma_f32 = gamma_dtype == KDKL_F32;
+  p.y_e4m3 = y_dtype == KDKL_E4M3;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = timed(kTNorm, s, [&] { return launch_rmsnorm(p, dv.sms, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "RMS norm launch");
+  return ok();
+}
+
+size_t kdkl_rmsnorm_workspace_bytes(int64_t N, int32_t d) {
+  if (check_norm(N, d, 0.f, KDKL_BF16, KDKL_BF16) != KDKL_OK) return 0;
+  return norm_part_bytes(N, d);
+}
+
+kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gamma, const void* dh, int64_t N,
+                                  int32_t d, float eps, int32_t h_dtype, int32_t gamma_dtype, void* dx,
+                                  float* dgamma, void* workspace, size_t workspace_bytes, void* stream) {
+  kdkl_status st = check_norm(N, d, eps, h_dtype, gamma_dtype);
+  if (st != KDKL_OK) return st;
+  if (!dy || !h || !gamma || !dx || !dgamma || !workspace)
+    return fail(KDKL_ERR_NULL, "dy, h, gamma, dx, dgamma and workspace must be non-NULL");
+  if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(gamma, 16) || !aligned(dh, 16) || !aligned(dx, 16))
+    return fail(KDKL_ERR_ALIGN, "dy, h, gamma, dh and dx must be 16-byte aligned");
+  if (!aligned(dgamma, 4)) return fail(KDKL_ERR_ALIGN, "dgamma must be 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(KDKL_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const size_t need = norm_part_bytes(N, d);
+  if (workspace_bytes < need) return fail(KDKL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  Device dv;
+  if ((st = current_device(dv)) != KDKL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    const cudaError_t e = cudaMemsetAsync(dgamma, 0, static_cast<size_t>(d) * 4, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    return ok();
+  }
+  NormGradParams p;
+  p.dy = dy;
+  p.h = h;
+  p.gamma = gamma;
+  p.dh = dh;
+  p.dx = dx;
+  p.part = static_cast<float*>(workspace);
+  p.N = N;
+  p.d = d;
+  p.eps = eps;
+  p.h_f32 = h_dtype == KDKL_F32;
+  p.gamma_f32 = gamma_dtype == KDKL_F32;
+  const int blocks = rmsnorm_grad_blocks(N, d, dv.sms);
+  const cudaError_t e = timed(kTNormGrad, s, [&] {
+    const cudaError_t e1 = launch_rmsnorm_grad(p, dv.sms, s);
+    return e1 != cudaSuccess ? e1 : launch_colsum(p.part, blocks, d, dgamma, s);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "RMS norm gradient launch");
+  return ok();
+}
+
+void kdkl_linear_options_init(kdkl_linear_options* options) {
+  if (options) *options = default_linear_options();
+}
+
+size_t kdkl_linear_workspace_bytes(int64_t M, int32_t d_in, int32_t d_out, int32_t backward) {
+  if (check_linear_shape(M, d_in, d_out, KDKL_BF16) != KDKL_OK) return 0;
+  return linear_layout(M, d_out, backward != 0).total;
+}
+
+kdkl_status kdkl_linear_plan(int64_t M, int32_t d_in, int32_t d_out, int32_t operands, int32_t product,
+                             int32_t sm_count, int32_t* plan_out) {
+  if (!plan_out) return fail(KDKL_ERR_NULL, "plan_out must be non-NULL");
+  kdkl_status st = check_linear_shape(M, d_in, d_out, operands);
+  if (st != KDKL_OK) return st;
+  if (product < KDKL_LINEAR_FORWARD || product > KDKL_LINEAR_DW)
+    return fail(KDKL_ERR_UNSUPPORTED, "unknown product %d", product);
+  if (product != KDKL_LINEAR_FORWARD && operands != KDKL_BF16)
+    return fail(KDKL_ERR_UNSUPPORTED, "KDKL_E4M3 operands have no gradient");
+  if (sm_count < 0 || sm_count == 1) return fail(KDKL_ERR_SHAPE, "sm_count must be 0 or >= 2");
+  if (sm_count == 0) {
+    Device dv;
+    if ((st = device_with_pairs(dv)) != KDKL_OK) return st;
+    sm_count = dv.sms;
+  }
+  Plan p;
+  if (product == KDKL_LINEAR_FORWARD)
+    st = pick_plan(0, operands == KDKL_E4M3 ? kLinFwdE4M3 : kLinFwd, M, d_out, d_in, sm_count, "plan", p);
+  else if (product == KDKL_LINEAR_DX)
+    st = pick_plan(0, kLinDx, M, d_in, d_out, sm_count, "dx_plan", p);
+  else
+    st = pick_plan(0, kLinDw, d_out, d_in, M, sm_count, "dw_plan", p);
+  if (st != KDKL_OK) return st;
+  *plan_out = p.code();
+  return ok();
+}
+
+kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, const void* residual, int64_t M,
+                                int32_t d_in, int32_t d_out, const kdkl_linear_options* options, void* y, void* pre,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const kdkl_linear_options o = options ? *options : default_linear_options();
+  kdkl_status st = check_linear_shape(M, d_in, d_out, o.operands);
+  if (st != KDKL_OK) return st;
+  if ((st = check_activation(o.activation)) != KDKL_OK) return st;
+  if (!x || !W || !y || !workspace) return fail(KDKL_ERR_NULL, "x, W, y and workspace must be non-NULL");
+  const bool f8 = o.operands == KDKL_E4M3;
+  if (f8 && (!o.x_scale || !o.w_scale)) return fail(KDKL_ERR_NULL, "KDKL_E4M3 operands need x_scale and w_scale");
+  if (!f8 && (o.x_scale || o.w_scale)) return fail(KDKL_ERR_UNSUPPORTED, "x_scale and w_scale go with KDKL_E4M3 operands only");
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) ||
+      !aligned(pre, 16))
+    return fail(KDKL_ERR_ALIGN, "x, W, bias, residual, y and pre must be 16-byte aligned");
+  if (!aligned(o.x_scale, 4) || !aligned(o.w_scale, 16))
+    return fail(KDKL_ERR_ALIGN, "x_scale must be 4-byte and w_scale 16-byte aligned");
+  if (!aligned(workspace, 256)) return fail(KDKL_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const LinearLayout L = linear_layout(M, d_out, false);
+  if (workspace_bytes < L.total) return fail(KDKL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+  Device dv;
+  if ((st = device_with_pairs(dv)) != KDKL_OK) return st;
+  const LinOp op = f8 ? kLinFwdE4M3 : kLinFwd;
+  Plan plan;
+  if ((st = pick_plan(o.plan, op, M, d_out, d_in, dv.sms, "plan", plan)) != KDKL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    return ok();
+  }
+  if ((st = debug_clear(workspace, s)) != KDKL_OK) return st;
+  LinParams p = {};
+  p.bias = static_cast<const uint16_t*>(bias);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.x_scale = o.x_scale;
+  p.w_scale = o.w_scale;
+  p.out = static_cast<uint16_t*>(y);
+  p.pre = static_cast<uint16_t*>(pre);
+  p.act = o.activation;
+  p.flags = static_cast<uint32_t*>(workspace);
+  p.clear_flags = 1;
+  const cudaError_t e = timed(kTLinear, s, [&] { return run_product(op, plan, x, W, M, d_out, d_in, p, dv.sms, s); });
+  if (e != cudaSuccess) return cuda_fail(e, "linear launch");
+  return ok();
+}
+
+kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x, const void* W, int64_t M,
+                                 int32_t d_in, int32_t d_out, const kdkl_linear_options* options, void* dx, void* dW,
+                                 float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  const kdkl_linear_options o = options ? *options : default_linear_options();
+  kdkl_status st = check_linear_shape(M, d_in, d_out, o.operands);
+  if (st != KDKL_OK) return st;
+  if (o.operands != KDKL_BF16) return fail(KDKL_ERR_UNSUPPORTED, "KDKL_E4M3 operands have no gradient");
+  if ((st = check_activation(o.activation)) != KDKL_OK) return st;
+  if (!dx && !dW && !dbias) return fail(KDKL_ERR_NULL, "one of dx, dW and dbias must be non-NULL");
+  if (!dy || !workspace) return fail(KDKL_ERR_NULL, "dy and workspace must be non-NULL");
+  if (dx && !W) return fail(KDKL_ERR_NULL, "dx needs W");
+  if (dW && !x) return fail(KDKL_ERR_NULL, "dW needs x");
+  const bool act = o.activation != KDKL_ACT_NONE;
+  if (act && !pre) return fail(KDKL_ERR_NULL, "the activation's gradient needs pre");
+  if (!aligned(dy, 16) || !aligned(pre, 16) || !aligned(x, 16) || !aligned(W, 16) || !aligned(dx, 16) ||
+      !aligned(dW, 16))
+    return fail(KDKL_ERR_ALIGN, "dy, pre, x, W, dx and dW must be 16-byte aligned");
+  if (!aligned(dbias, 4)) return fail(KDKL_ERR_ALIGN, "dbias must be 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(KDKL_ERR_ALIGN, "workspace must be 256-byte aligned");
+  const LinearLayout L = linear_layout(M, d_out, true);
+  if (workspace_bytes < L.total) return fail(KDKL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+  Device dv;
+  if ((st = device_with_pairs(dv)) != KDKL_OK) return st;
+  if (dv.sms > kMaxSms) return fail(KDKL_ERR_UNSUPPORTED, "a device with %d SMs", dv.sms);
+  Plan dx_plan, dw_plan;
+  if (dx && (st = pick_plan(o.dx_plan, kLinDx, M, d_in, d_out, dv.sms, "dx_plan", dx_plan)) != KDKL_OK) return st;
+  if (dW && (st = pick_plan(o.dw_plan, kLinDw, d_out, d_in, M, dv.sms, "dw_plan", dw_plan)) != KDKL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(workspace, 0, kFlagBytes, s)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+  if (M == 0) {
+    if (dW && (e = cudaMemsetAsync(dW, 0, static_cast<size_t>(d_out) * d_in * 2, s)) != cudaSuccess)
+      return cuda_fail(e, "cudaMemsetAsync");
+    if (dbias && (e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(d_out) * 4, s)) != cudaSuccess)
+      return cuda_fail(e, "cudaMemsetAsync");
+    return ok();
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* dz = dy;
+  if (act || dbias) {
+    uint16_t* dz_out = act && (dx || dW) ? reinterpret_cast<uint16_t*>(ws + L.dz) : nullptr;
+    float* part = dbias ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+    const int chunks = act_grad_chunks(M, d_out, dv.sms);
+    e = timed(kTActGrad, s, [&] {
+      const cudaError_t e1 = launch_act_grad(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre),
+                                             o.activation, M, d_out, dz_out, part, chunks, s);
+      return e1 != cudaSuccess || !dbias ? e1 : launch_colsum(part, chunks, d_out, dbias, s);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
+    if (act) dz = ws + L.dz;
+  }
+  LinParams p = {};
+  p.flags = static_cast<uint32_t*>(workspace);
+  if (dx) {
+    p.out = static_cast<uint16_t*>(dx);
+    e = timed(kTLinearDx, s, [&] { return run_product(kLinDx, dx_plan, dz, W, M, d_in, d_out, p, dv.sms, s); });
+    if (e != cudaSuccess) return cuda_fail(e, "linear dx launch");
+  }
+  if (dW) {
+    p.out = static_cast<uint16_t*>(dW);
+    e = timed(kTLinearDw, s, [&] { return run_product(kLinDw, dw_plan, dz, x, d_out, d_in, M, p, dv.sms, s); });
+    if (e != cudaSuccess) return cuda_fail(e, "linear dW launch");
+  }
+  return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,95 @@
+// Internal declarations of the operators ahead of the output head (RMS norm and linear layer):
+// launchers defined in norm.cu and linear.cu, called by layer_api.cu.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace kdkl {
+
+// ---------------------------------------------------------------- RMS norm (norm.cu)
+// A row is held in the registers of one warp or one block, kNormVec elements per thread and step.
+constexpr int kNormVec = 8;
+constexpr int kNormMaxThreads = 512;
+constexpr int kNormMaxD = kNormMaxThreads * kNormVec * 8;   // 8 steps of kNormVec elements per thread
+// Blocks of the gradient kernel, each leaving one row of partial sums for dgamma.
+constexpr int kNormGradBlocks = 592;
+
+struct NormParams {
+  const void* x;
+  const void* residual;   // may be null
+  const void* gamma;
+  void* h;                // may be null
+  void* y;
+  float* y_scale;         // e4m3 output only
+  int64_t N;
+  int d;
+  float eps;
+  bool x_f32, h_f32, gamma_f32, y_e4m3;
+};
+cudaError_t launch_rmsnorm(const NormParams& p, int sms, cudaStream_t s);
+
+struct NormGradParams {
+  const void* dy;         // bf16
+  const void* h;
+  const void* gamma;
+  const void* dh;         // may be null
+  void* dx;
+  float* part;            // [blocks, d]
+  int64_t N;
+  int d;
+  float eps;
+  bool h_f32, gamma_f32;
+};
+// Blocks (rows of `part`) that launch_rmsnorm_grad uses.
+int rmsnorm_grad_blocks(int64_t N, int d, int sms);
+cudaError_t launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s);
+
+// out[c] = sum over rows of part[rows, n], in a fixed order.
+cudaError_t launch_colsum(const float* part, int rows, int n, float* out, cudaStream_t s);
+
+// ---------------------------------------------------------------- linear layer (linear.cu)
+// Operand layouts and epilogues of the products:
+//   kLinFwd     y = act(x W^T + b) + r, bf16      A = x K-major,   B = W K-major
+//   kLinFwdE4M3 the same from e4m3 operands       A = x K-major,   B = W K-major
+//   kLinDx      dx = dz W                         A = dz K-major,  B = W MN-major
+//   kLinDw      dW = dz^T x                       A = dz MN-major, B = x MN-major
+enum LinOp { kLinFwd = 0, kLinFwdE4M3 = 1, kLinDx = 2, kLinDw = 3 };
+
+struct LinParams {
+  int M;                 // rows of the output
+  int N;                 // columns of the output
+  int k_blocks;          // 128-byte reduction blocks (dz and x as MN-major operands: 64 rows)
+  int units;             // output tiles
+  int n_tiles;           // tiles along N
+  int row_group;         // row blocks swept together (large tiles)
+  int splits;            // reduction splits = cluster size (small tiles)
+  const uint16_t* bias;      // [N] bf16 or null
+  const uint16_t* residual;  // [M, N] bf16 or null
+  const float* x_scale;      // [M] or null
+  const float* w_scale;      // [N] or null
+  uint16_t* out;         // [M, N] bf16 (small tiles; large tiles store through a tensor map)
+  uint16_t* pre;         // [M, N] bf16 or null
+  int act;
+  uint32_t* flags;       // device flag word
+  int clear_flags;       // the first block zeroes the flag word
+};
+
+// Large tiles: 256 x bn (bn = 256, 192 or 128) by CTA pairs, persistent.
+cudaError_t launch_linear_pair(int op, int bn, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                               const CUtensorMap& tmOut, const CUtensorMap& tmPre, const LinParams& p, int grid,
+                               cudaStream_t s);
+// Small tiles: 128 output columns x nt rows (nt = 16, 32, 64 or 128) per cluster of p.splits CTAs; the
+// roles of the operands are swapped (tmA reads W, tmB reads x or dz).  op: all but kLinDw.
+cudaError_t launch_linear_small(int op, int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
+                                cudaStream_t s);
+
+// dz = dy * act'(pre) in bf16 (dz may be null: column sums only, of dy when act is none) and the
+// partial column sums part[chunks, n] of its fp32 values (part may be null).
+constexpr int kMaxSms = 512;   // workspaces are sized for any device up to this many SMs
+int act_grad_chunks(int64_t M, int n, int sms);
+cudaError_t launch_act_grad(const uint16_t* dy, const uint16_t* pre, int act, int64_t M, int n, uint16_t* dz,
+                            float* part, int chunks, cudaStream_t s);
+
+}  // namespace kdkl

@@ -1,0 +1,846 @@
+// Linear layer with bias, activation and residual in its epilogue, and its gradient (sm_100a).
+//
+//   forward   z = x W^T + b,  y = act(z) + r           x [M, d_in], W [d_out, d_in], y [M, d_out]
+//   gradient  dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_rows dz
+//
+// Two tcgen05 kernels share the operand layouts (128-byte swizzled tiles fetched by TMA):
+//
+//   linear_pair_kernel   256 x BN output tiles by CTA pairs (cta_group::2), persistent, two accumulators
+//                        in TMEM so that the epilogue of one tile runs under the next tile's MMAs.
+//   linear_small_kernel  few rows: the operands swap roles, so that 128 rows of W fill the MMA's M and the
+//                        rows of x its N (16 to 128), and a cluster of CTAs splits the reduction and joins
+//                        the partial tiles over distributed shared memory in a fixed order.  The weights
+//                        stream through all SMs at once however few the rows are.
+//
+// Sums are held in fp32 (TMEM accumulators, fp32 joins); z is rounded to bf16 only where it is
+// stored, and dz once, as the MMA operand of both gradient products.
+#include <atomic>
+#include <cmath>
+
+#include "../../include/kdkl.h"
+#include "kdkl_internal.h"
+#include "layer_internal.h"
+#include "sm100.cuh"
+
+namespace kdkl {
+namespace {
+
+constexpr float kLog2eL = 1.4426950408889634f;
+
+// ---------------------------------------------------------------- activations
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 1 / (1 + e^-z).  The hardware exponential and reciprocal are within 2 ulp each, far below the
+// bf16 rounding of the results; for z below -88 the exponential is inf and the result 0.
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2eL * z)); }
+
+// 2 u of the tanh form of GELU: 0.5 (1 + tanh u) = sigmoid(2 u).
+__device__ __forceinline__ float gelu_2u(float z) { return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z); }
+
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+  if (ACT == KDKL_ACT_RELU) return z < 0.f ? 0.f : z;   // NaN passes
+  if (ACT == KDKL_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (ACT == KDKL_ACT_GELU_TANH) return z * sigmoid_f(gelu_2u(z));
+  if (ACT == KDKL_ACT_SILU) return z * sigmoid_f(z);
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_grad_f(float z) {
+  if (ACT == KDKL_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);   // NaN passes
+  if (ACT == KDKL_ACT_GELU) {
+    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+    return fmaf(z * 0.3989422804014327f, ex2_approx(-0.5f * kLog2eL * z * z), cdf);
+  }
+  if (ACT == KDKL_ACT_GELU_TANH) {
+    const float p = sigmoid_f(gelu_2u(z));
+    return fmaf(z * p * (1.0f - p), 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.0f), p);
+  }
+  if (ACT == KDKL_ACT_SILU) {
+    const float p = sigmoid_f(z);
+    return fmaf(z * p, 1.0f - p, p);
+  }
+  return 1.0f;
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_each(float (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = act_f<ACT>(v[j]);
+}
+
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+  switch (act) {
+    case KDKL_ACT_RELU: act_each<KDKL_ACT_RELU>(v); break;
+    case KDKL_ACT_GELU: act_each<KDKL_ACT_GELU>(v); break;
+    case KDKL_ACT_GELU_TANH: act_each<KDKL_ACT_GELU_TANH>(v); break;
+    case KDKL_ACT_SILU: act_each<KDKL_ACT_SILU>(v); break;
+    default: break;
+  }
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// ---------------------------------------------------------------- PTX of these kernels
+// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (both K-major) and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <bool F8, bool PAIR>
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+  if (!F8) {
+    if (PAIR) umma_bf16_pair(d_tmem, ad, bd, idesc, acc);
+    else umma_bf16(d_tmem, ad, bd, idesc, acc);
+  } else if (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+
+// 32 lanes x 16 consecutive 32-bit columns: thread i of the warp gets lane (base + i).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4f(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// Operand layout of a product: element type and which operands are MN-major.
+template <int OP>
+struct LinLayout {
+  static constexpr bool kF8 = OP == kLinFwdE4M3;
+  static constexpr bool kFull = OP == kLinFwd || OP == kLinFwdE4M3;   // scales, bias, activation, residual
+  static constexpr int kStepElems = kF8 ? 128 : 64;                   // elements of one 128-byte reduction block
+};
+
+// Zeroes the flag word before any of this launch's waits can time out (they take kWaitLimitNs at
+// least; the bounds-checking build, whose checks can fail at once, clears it ahead of the launch).
+__device__ __forceinline__ void clear_flags(const LinParams& p) {
+#ifndef KDKL_DEBUG
+  if (p.clear_flags && blockIdx.x == 0 && threadIdx.x == 0) *p.flags = 0u;
+#endif
+}
+
+// ============================================================================
+// large tiles: one 256 x BN tile per CTA pair and turn
+//
+// Warp 0 issues the TMA loads, warp 1 of the even CTA the MMAs, and eight epilogue warps read TMEM (two
+// per 32-lane quarter, each half of the tile's columns).  Tiles are swept in groups of row_group row
+// blocks, column by column, so that the pairs running at once share their A rows and B columns in L2.
+// ============================================================================
+constexpr int kPairThreads = 320;
+constexpr int kEpiWarps = 8;
+
+template <int OP, int BN>
+struct PairCfg {
+  using L = LinLayout<OP>;
+  static constexpr bool kAmn = OP == kLinDw;
+  static constexpr bool kBmn = OP == kLinDx || OP == kLinDw;
+  static constexpr int kCtaN = BN / 2;                      // B rows held by each CTA of the pair
+  static constexpr int kBAtoms = (kCtaN + 63) / 64;         // MN-major B: whole 64-column swizzle atoms
+  static constexpr int kABytes = kBM * 128;
+  static constexpr int kBBytes = kBmn ? kBAtoms * 8192 : kCtaN * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kTxBytes = 2 * kStageBytes;          // both CTAs' bytes, counted on the even CTA
+  static constexpr int kEpiWarpBytes = 2 * 2048;            // two 32 x 32 bf16 staging buffers
+  static constexpr int kEpiBytes = kEpiWarps * kEpiWarpBytes;
+  static constexpr int kStagesFit = (232448 - 1024 - kEpiBytes - 512) / kStageBytes;
+  static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 512;
+  static constexpr uint32_t kIdesc = L::kF8 ? idesc_e4m3_f32(256, BN) : idesc_bf16_f32(256, BN, kAmn, kBmn);
+  static constexpr int kAccStride = BN <= 128 ? 128 : 256;
+  static constexpr uint32_t kTmemCols = 2 * kAccStride;
+  static_assert(BN % 64 == 0 && BN >= 128 && BN <= 256, "two halves of whole 32-column chunks");
+  static_assert(kStages >= 4 && (2 * kStages + 5) * 8 + 16 <= 512, "stages");
+};
+
+__device__ __forceinline__ void lin_tile(const LinParams& p, int u, int& mb, int& t) {
+  const int rows = p.units / p.n_tiles;
+  const int g = u / (p.row_group * p.n_tiles);
+  const int r0 = g * p.row_group;
+  const int rg = min(p.row_group, rows - r0);
+  const int off = u - r0 * p.n_tiles;
+  t = off / rg;
+  mb = r0 + off - t * rg;
+}
+
+template <int OP, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre,
+                       const LinParams p) {
+  using C = PairCfg<OP, BN>;
+  using L = LinLayout<OP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::kStages * C::kABytes;
+  uint8_t* sEpi = sB + C::kStages * C::kBBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::kEpiBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();   // 0 = the CTA that issues the MMAs
+  const int group = static_cast<int>(blockIdx.x >> 1), ngroups = static_cast<int>(gridDim.x >> 1);
+
+  clear_flags(p);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();   // the even CTA's barriers are initialised before any peer signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const AbortState ab{abort_flag, p.flags};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool wrapped = false, stop = false;
+      for (int u = group; u < p.units && !stop; u += ngroups) {
+        int mb, t;
+        lin_tile(p, u, mb, t);
+        const int arow = mb * 256 + static_cast<int>(rank) * kBM;
+        const int brow = t * BN + static_cast<int>(rank) * C::kCtaN;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, ab)) {
+            stop = true;
+            break;
+          }
+          uint8_t* a = sA + stage * C::kABytes;
+          uint8_t* b = sB + stage * C::kBBytes;
+          const uint32_t bar0 = mapa_shared(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::kTxBytes);
+          if (C::kAmn) {
+            tma_load_2d_pair(a, &tmA, bar0, arow, kb * 64);
+            tma_load_2d_pair(a + 8192, &tmA, bar0, arow + 64, kb * 64);
+          } else {
+            tma_load_2d_pair(a, &tmA, bar0, kb * L::kStepElems, arow);
+          }
+          if (C::kBmn) {
+#pragma unroll
+            for (int q = 0; q < C::kBAtoms; ++q)
+              tma_load_2d_pair(b + q * 8192, &tmB, bar0, brow + q * 64, kb * 64);
+          } else {
+            tma_load_2d_pair(b, &tmB, bar0, kb * L::kStepElems, brow);
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+            wrapped = true;
+          }
+        }
+      }
+      if (rank == 0 && *abort_flag) {
+        // giving up: wait (bounded) until the copies already issued have landed
+        const uint64_t w0 = globaltimer_ns();
+        for (int s2 = 0; s2 < C::kStages; ++s2) {
+          if (!wrapped && s2 >= stage) break;
+          const uint32_t par = s2 < stage ? phase : (phase ^ 1u);
+          while (!mbar_try_wait(smem_u32(&full[s2]), par) && globaltimer_ns() - w0 < kDrainLimitNs) {
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA only)
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int u = group; u < p.units; u += ngroups) {
+        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, ab)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAccStride);
+        bool got = true;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          got = mbar_wait(&full[stage], phase, ab);
+          if (!got) break;
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(sA + stage * C::kABytes);
+          const uint32_t b_addr = smem_u32(sB + stage * C::kBBytes);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {   // 32 bytes of the reduction axis (16 bf16 or 32 e4m3) per MMA
+            const uint64_t ad = C::kAmn ? sdesc_sw128(a_addr + j * 2048, 8192, 1024)
+                                        : sdesc_sw128(a_addr + j * 32, 16, 1024);
+            const uint64_t bd = C::kBmn ? sdesc_sw128(b_addr + j * 2048, 8192, 1024)
+                                        : sdesc_sw128(b_addr + j * 32, 16, 1024);
+            umma<L::kF8, true>(d_tmem, ad, bd, C::kIdesc, (kb | j) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair(&empty[stage], 0x3);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!got) break;
+        umma_commit_pair(&acc_full[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      // every MMA issued above has finished before TMEM or shared memory is released
+      umma_commit_pair(drain, 0x1);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(drain), 0)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          atomicOr(p.flags, kFlagTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue warps
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
+    uint8_t* wbuf = sEpi + (warp - 2) * C::kEpiWarpBytes;
+    int sbuf = 0, acc = 0;
+    uint32_t acc_phase = 0;
+    // stages 32 rows x 32 bf16 columns (64-byte swizzle) and stores them by TMA, which clips the
+    // columns past N and the rows past M
+    auto store32 = [&](const CUtensorMap* tm, const float(&v)[32], int col, int row) {
+      uint8_t* buf = wbuf + sbuf * 2048;
+      if (lane == 0) bulk_wait_read<1>();   // the store before last has read this buffer
+      __syncwarp();
+      const uint32_t sw = static_cast<uint32_t>((lane >> 1) & 3);
+      const uint32_t row_addr = smem_u32(buf) + static_cast<uint32_t>(lane) * 64u;
+#pragma unroll
+      for (int c16 = 0; c16 < 4; ++c16)
+        st_shared_v4(row_addr + ((static_cast<uint32_t>(c16) ^ sw) << 4),
+                     pack_bf16x2(v[c16 * 8 + 0], v[c16 * 8 + 1]), pack_bf16x2(v[c16 * 8 + 2], v[c16 * 8 + 3]),
+                     pack_bf16x2(v[c16 * 8 + 4], v[c16 * 8 + 5]), pack_bf16x2(v[c16 * 8 + 6], v[c16 * 8 + 7]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && dbg_ok((col & 7) == 0 && col >= 0 && row >= 0, p.flags)) {
+        tma_store_2d(tm, buf, col, row);
+        bulk_commit();
+      }
+      sbuf ^= 1;
+    };
+    for (int u = group; u < p.units; u += ngroups) {
+      int mb, t;
+      lin_tile(p, u, mb, t);
+      const int row0 = mb * 256 + static_cast<int>(rank) * kBM + q * 32;   // the warp's first row
+      const int row = row0 + lane;
+      const int c_first = t * BN + half * (BN / 2);
+      uint4 res[4];
+      float xs = 1.f;
+      const bool has_res = L::kFull && p.residual != nullptr && row < p.M;
+      auto load_res = [&](int col) {
+        const uint16_t* src = p.residual + static_cast<int64_t>(row) * p.N + col;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (col + g * 8 < p.N) res[g] = *reinterpret_cast<const uint4*>(src + g * 8);
+      };
+      if (L::kFull) {
+        // fetched while the tile's MMAs run
+#pragma unroll
+        for (int g = 0; g < 4; ++g) res[g] = make_uint4(0u, 0u, 0u, 0u);
+        if (has_res && c_first < p.N) load_res(c_first);
+        if (L::kF8 && row < p.M) xs = p.x_scale[row];
+      }
+      if (!mbar_wait(&acc_full[acc], acc_phase, ab)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + lane_addr + static_cast<uint32_t>(acc * C::kAccStride + half * (BN / 2));
+#pragma unroll 1
+      for (int c = 0; c < BN / 64; ++c) {
+        const int col = c_first + c * 32;
+        if (col >= p.N) break;
+        float v[32];
+        tmem_ld32(tbase + c * 32, v);
+        tmem_wait_ld();
+        if (L::kFull) {
+          if (L::kF8) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              if (col + g * 4 < p.N) {
+                const float4 w = *reinterpret_cast<const float4*>(p.w_scale + col + g * 4);
+                v[g * 4 + 0] *= xs * w.x;
+                v[g * 4 + 1] *= xs * w.y;
+                v[g * 4 + 2] *= xs * w.z;
+                v[g * 4 + 3] *= xs * w.w;
+              }
+          }
+          if (p.bias) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (col + g * 8 < p.N) {
+                const uint4 b = *reinterpret_cast<const uint4*>(p.bias + col + g * 8);
+                v[g * 8 + 0] += bf_lo(b.x), v[g * 8 + 1] += bf_hi(b.x);
+                v[g * 8 + 2] += bf_lo(b.y), v[g * 8 + 3] += bf_hi(b.y);
+                v[g * 8 + 4] += bf_lo(b.z), v[g * 8 + 5] += bf_hi(b.z);
+                v[g * 8 + 6] += bf_lo(b.w), v[g * 8 + 7] += bf_hi(b.w);
+              }
+          }
+          if (p.pre) store32(&tmPre, v, col, row0);
+          act_all(v, p.act);
+          if (p.residual) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              v[g * 8 + 0] += bf_lo(res[g].x), v[g * 8 + 1] += bf_hi(res[g].x);
+              v[g * 8 + 2] += bf_lo(res[g].y), v[g * 8 + 3] += bf_hi(res[g].y);
+              v[g * 8 + 4] += bf_lo(res[g].z), v[g * 8 + 5] += bf_hi(res[g].z);
+              v[g * 8 + 6] += bf_lo(res[g].w), v[g * 8 + 7] += bf_hi(res[g].w);
+            }
+            if (has_res && c + 1 < BN / 64 && col + 32 < p.N) load_res(col + 32);
+          }
+        }
+        store32(&tmOut, v, col, row0);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty0 + static_cast<uint32_t>(acc) * 8u);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  if (*abort_flag) {
+    // give copies that may still be landing in shared memory time to finish
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // the peer's shared memory and TMEM stay alive until the pair is done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, C::kTmemCols);
+  }
+}
+
+// ============================================================================
+// small tiles: 128 output columns x NT rows per cluster, the reduction split over its CTAs
+//
+// A = 128 rows of W (for dx: 128 columns of W, MN-major), B = NT rows of x (or dz).  Each CTA reduces its
+// share of the reduction blocks into a [128 x NT] TMEM tile, spills it to shared memory as [row][column]
+// fp32, and after a cluster barrier each CTA joins and finishes 1 / splits of the tile: for every output it
+// adds the partial sums in CTA order.  No workspace, no atomics, one launch.
+// ============================================================================
+constexpr int kSmallThreads = 192;
+
+template <int OP, int NT>
+struct SmallCfg {
+  using L = LinLayout<OP>;
+  static constexpr bool kAmn = OP == kLinDx;
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = NT * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  // about 100 KB of stages, so that two CTAs share an SM and one's set-up and join hide under the other's loads
+  static constexpr int kStages = NT <= 32 ? 5 : (NT == 64 ? 4 : 3);
+  static constexpr int kTileBytes = NT * 128 * 4;           // the partial tile, over the drained stages
+  static constexpr int kDataBytes = kStages * kStageBytes;
+  static constexpr int kSmem = 1024 + kDataBytes + 256;
+  static constexpr uint32_t kIdesc = L::kF8 ? idesc_e4m3_f32(128, NT) : idesc_bf16_f32(128, NT, kAmn, false);
+  static constexpr uint32_t kTmemCols = NT < 32 ? 32u : static_cast<uint32_t>(NT);
+  static_assert(kTileBytes <= kDataBytes, "the partial tile fits the stages");
+  static_assert(NT % 16 == 0 && NT >= 16 && NT <= 128, "NT");
+};
+
+template <int OP, int NT>
+__global__ void __launch_bounds__(kSmallThreads)
+    linear_small_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const LinParams p) {
+  using C = SmallCfg<OP, NT>;
+  using L = LinLayout<OP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::kStages * C::kABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kDataBytes);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* done = empty + C::kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int tile = static_cast<int>(blockIdx.x) / p.splits;
+  const int row_tiles = (p.M + NT - 1) / NT;
+  const int ct = tile / row_tiles, rt = tile - ct * row_tiles;   // row tiles of one column tile run together
+  const int col0 = ct * 128, row0 = rt * NT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
+
+  clear_flags(p);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const AbortState ab{abort_flag, p.flags};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, ab)) break;
+        uint8_t* a = sA + stage * C::kABytes;
+        mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+        if (C::kAmn) {
+          tma_load_2d(a, &tmA, &full[stage], col0, kb * 64);
+          tma_load_2d(a + 8192, &tmA, &full[stage], col0 + 64, kb * 64);
+        } else {
+          tma_load_2d(a, &tmA, &full[stage], kb * L::kStepElems, col0);
+        }
+        tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * L::kStepElems, row0);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[stage], phase, ab)) break;
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(sA + stage * C::kABytes);
+        const uint32_t b_addr = smem_u32(sB + stage * C::kBBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t ad = C::kAmn ? sdesc_sw128(a_addr + j * 2048, 8192, 1024)
+                                      : sdesc_sw128(a_addr + j * 32, 16, 1024);
+          umma<L::kF8, false>(tmem_base, ad, sdesc_sw128(b_addr + j * 32, 16, 1024), C::kIdesc,
+                              (kb != kb0 || j != 0) ? 1u : 0u);
+        }
+        umma_commit(&empty[stage]);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      umma_commit(done);
+    }
+    __syncwarp();
+  }
+  // Every MMA has read its operands once `done` completes, and every load was waited for by an MMA, so
+  // the stages can be overwritten (on the abort path copies may still be landing: nothing is written).
+  const bool good = mbar_wait(done, 0, ab) && !*abort_flag;
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(smem);   // [NT][128]
+  if (warp >= 2 && good) {
+    const int f = (warp & 3) * 32 + lane;         // output column of this thread's TMEM lane
+    const uint32_t tbase = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll 1
+    for (int j0 = 0; j0 < NT; j0 += 16) {
+      if (row0 + j0 >= p.M) break;
+      float v[16];
+      tmem_ld16(tbase + j0, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) part[(j0 + j) * 128 + f] = v[j];
+    }
+  }
+  if (!good) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kDrainLimitNs) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+  if (good) {
+    const int rows = min(NT, p.M - row0);
+    const int items = rows * 32;                  // groups of four columns
+    const int i0 = static_cast<int>(static_cast<int64_t>(items) * rank / p.splits);
+    const int i1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / p.splits);
+    const uint32_t base = smem_u32(part);
+    for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kSmallThreads) {
+      const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
+      if (col >= p.N) continue;
+      const int64_t at = static_cast<int64_t>(row) * p.N + col;
+      uint2 res = make_uint2(0u, 0u);
+      if (L::kFull && p.residual) res = *reinterpret_cast<const uint2*>(p.residual + at);
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 q = ld_cluster_v4f(mapa_shared(base + static_cast<uint32_t>(i) * 16u, s));
+        v[0] += q.x;
+        v[1] += q.y;
+        v[2] += q.z;
+        v[3] += q.w;
+      }
+      if (L::kFull) {
+        if (L::kF8) {
+          const float xs = p.x_scale[row];
+          const float4 w = *reinterpret_cast<const float4*>(p.w_scale + col);
+          v[0] *= xs * w.x;
+          v[1] *= xs * w.y;
+          v[2] *= xs * w.z;
+          v[3] *= xs * w.w;
+        }
+        if (p.bias) {
+          const uint2 b = *reinterpret_cast<const uint2*>(p.bias + col);
+          v[0] += bf_lo(b.x), v[1] += bf_hi(b.x), v[2] += bf_lo(b.y), v[3] += bf_hi(b.y);
+        }
+        if (p.pre)
+          *reinterpret_cast<uint2*>(p.pre + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        act_all(v, p.act);
+        if (p.residual) {
+          v[0] += bf_lo(res.x), v[1] += bf_hi(res.x), v[2] += bf_lo(res.y), v[3] += bf_hi(res.y);
+        }
+      }
+      *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+  }
+  __syncwarp();
+  cluster_sync();   // this CTA's partial tile stays readable until every peer has joined its share
+}
+
+// ============================================================================
+// dz = dy act'(pre), bf16, and partial column sums of its fp32 values
+//
+// One block: 256 columns (8 per thread) x a range of rows, eight rows at a time.
+// ============================================================================
+constexpr int kActRows = 8;
+
+template <int ACT>
+__global__ void __launch_bounds__(32 * kActRows)
+    act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ pre, int64_t M, int n,
+                    uint16_t* __restrict__ dz, float* __restrict__ part) {
+  __shared__ float s[kActRows][32][9];
+  const int col = (static_cast<int>(blockIdx.x) * 32 + static_cast<int>(threadIdx.x)) * 8;
+  const int64_t r0 = M * blockIdx.y / gridDim.y, r1 = M * (blockIdx.y + 1) / gridDim.y;
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+  if (col < n) {
+#pragma unroll 4
+    for (int64_t r = r0 + threadIdx.y; r < r1; r += kActRows) {
+      const int64_t at = r * n + col;
+      const uint4 g = *reinterpret_cast<const uint4*>(dy + at);
+      float v[8] = {bf_lo(g.x), bf_hi(g.x), bf_lo(g.y), bf_hi(g.y), bf_lo(g.z), bf_hi(g.z), bf_lo(g.w), bf_hi(g.w)};
+      if (ACT != KDKL_ACT_NONE) {
+        const uint4 z = *reinterpret_cast<const uint4*>(pre + at);
+        const float w[8] = {bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y),
+                            bf_lo(z.z), bf_hi(z.z), bf_lo(z.w), bf_hi(z.w)};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(w[j]);
+        if (dz)
+          *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[threadIdx.y][threadIdx.x][j] = acc[j];
+  __syncthreads();
+  const int c = static_cast<int>(threadIdx.y) * 32 + static_cast<int>(threadIdx.x);   // one column each
+  const int out = static_cast<int>(blockIdx.x) * 256 + c;
+  if (out < n) {
+    float t = 0.f;
+#pragma unroll
+    for (int r = 0; r < kActRows; ++r) t += s[r][c >> 3][c & 7];
+    part[static_cast<int64_t>(blockIdx.y) * n + out] = t;
+  }
+}
+
+// Sets a kernel's dynamic shared-memory limit on its first launch on each device (devices past the 64th:
+// on every launch).
+template <class K>
+cudaError_t configure(K* kernel, int smem, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
+cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, int smem, unsigned cluster, cudaStream_t s,
+                                  cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int OP, int BN>
+cudaError_t pair_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
+                     const CUtensorMap& tmPre, const LinParams& p, int grid, cudaStream_t s) {
+  using C = PairCfg<OP, BN>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = configure(linear_pair_kernel<OP, BN>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(grid), kPairThreads, C::kSmem, 2, s, &attr);
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OP, BN>, tmA, tmB, tmOut, tmPre, p);
+}
+
+template <int OP>
+cudaError_t pair_op(int bn, const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
+                    const CUtensorMap& tmPre, const LinParams& p, int grid, cudaStream_t s) {
+  switch (bn) {
+    case 256: return pair_one<OP, 256>(tmA, tmB, tmOut, tmPre, p, grid, s);
+    case 192: return pair_one<OP, 192>(tmA, tmB, tmOut, tmPre, p, grid, s);
+    case 128: return pair_one<OP, 128>(tmA, tmB, tmOut, tmPre, p, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <int OP, int NT>
+cudaError_t small_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p, cudaStream_t s) {
+  using C = SmallCfg<OP, NT>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = configure(linear_small_kernel<OP, NT>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(tiles * p.splits), kSmallThreads, C::kSmem,
+                                                static_cast<unsigned>(p.splits), s, &attr);
+  return cudaLaunchKernelEx(&cfg, linear_small_kernel<OP, NT>, tmA, tmB, p);
+}
+
+template <int OP>
+cudaError_t small_op(int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p, cudaStream_t s) {
+  switch (nt) {
+    case 16: return small_one<OP, 16>(tmA, tmB, p, s);
+    case 32: return small_one<OP, 32>(tmA, tmB, p, s);
+    case 64: return small_one<OP, 64>(tmA, tmB, p, s);
+    case 128: return small_one<OP, 128>(tmA, tmB, p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pair(int op, int bn, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                               const CUtensorMap& tmOut, const CUtensorMap& tmPre, const LinParams& p, int grid,
+                               cudaStream_t s) {
+  switch (op) {
+    case kLinFwd: return pair_op<kLinFwd>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
+    case kLinFwdE4M3: return pair_op<kLinFwdE4M3>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
+    case kLinDx: return pair_op<kLinDx>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
+    case kLinDw: return pair_op<kLinDw>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_linear_small(int op, int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
+                                cudaStream_t s) {
+  switch (op) {
+    case kLinFwd: return small_op<kLinFwd>(nt, tmA, tmB, p, s);
+    case kLinFwdE4M3: return small_op<kLinFwdE4M3>(nt, tmA, tmB, p, s);
+    case kLinDx: return small_op<kLinDx>(nt, tmA, tmB, p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int act_grad_chunks(int64_t M, int n, int sms) {
+  const int64_t cols = (n + 255) / 256;
+  const int64_t want = (8 * static_cast<int64_t>(sms) + cols - 1) / cols;   // about eight blocks per SM
+  const int64_t most = (M + kActRows - 1) / kActRows;
+  const int64_t c = want < most ? want : most;
+  return static_cast<int>(c < 1 ? 1 : c);
+}
+
+cudaError_t launch_act_grad(const uint16_t* dy, const uint16_t* pre, int act, int64_t M, int n, uint16_t* dz,
+                            float* part, int chunks, cudaStream_t s) {
+  const dim3 grid((n + 255) / 256, chunks), block(32, kActRows);
+  switch (act) {
+    case KDKL_ACT_NONE: act_grad_kernel<KDKL_ACT_NONE><<<grid, block, 0, s>>>(dy, pre, M, n, dz, part); break;
+    case KDKL_ACT_RELU: act_grad_kernel<KDKL_ACT_RELU><<<grid, block, 0, s>>>(dy, pre, M, n, dz, part); break;
+    case KDKL_ACT_GELU: act_grad_kernel<KDKL_ACT_GELU><<<grid, block, 0, s>>>(dy, pre, M, n, dz, part); break;
+    case KDKL_ACT_GELU_TANH:
+      act_grad_kernel<KDKL_ACT_GELU_TANH><<<grid, block, 0, s>>>(dy, pre, M, n, dz, part);
+      break;
+    case KDKL_ACT_SILU: act_grad_kernel<KDKL_ACT_SILU><<<grid, block, 0, s>>>(dy, pre, M, n, dz, part); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace kdkl
