@@ -417,7 +417,7 @@ typedef enum {
 
 typedef struct {
   int32_t operands;      /* KDKL_BF16 (default) or KDKL_E4M3 */
-  int32_t activation;    /* kdkl_activation (default KDKL_ACT_NONE) */
+  int32_t activation;    /* a kdkl_activation; default KDKL_ACT_NONE */
   const float* x_scale;  /* KDKL_E4M3: [M] fp32 */
   const float* w_scale;  /* KDKL_E4M3: [d_out] fp32 */
   /* Tiles of the products: 0 = the planner's choice (default), else a plan as kdkl_linear_plan reports it.
