@@ -177,7 +177,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -375,37 +376,37 @@ def _bad(status: int, where: str, detail: str):
     raise KDKLError(status, where, detail)
 
 
-def _tensor(where, name, t, shape, dtypes, device) -> int | None:
+def _tensor(where, name, t, shape, dtypes, dev) -> int | None:
     """Address of a tensor argument after checking its shape, type, layout and device (None stays None)."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.shape != shape:
         _bad(2, where, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
         _bad(4, where, f"{name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if not t.is_contiguous():
         _bad(2, where, f"{name} must be dense row-major")
-    if t.device != device:
-        _bad(4, where, f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr()
+    _bad(4, where, f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _where(where, t, name):
-    """The current device, after checking that `t`, a CUDA tensor of two dimensions, is on it."""
+    """torch and the current device's index, after checking that `t`, of two dimensions, is on that device."""
     import torch
     if t.dim() != 2:
         _bad(2, where, f"{name} has {t.dim()} dimensions, expected 2")
-    dev = t.device
-    if dev.type != "cuda":
-        _bad(4, where, f"{name} is on {dev}, expected the current CUDA device")
-    if dev.index != torch.cuda.current_device():
-        _bad(4, where, f"{name} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    dev = t.get_device()
+    if dev < 0:
+        _bad(4, where, f"{name} is on {t.device}, expected the current CUDA device")
+    if dev != torch.cuda.current_device():
+        _bad(4, where, f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return torch, dev
 
 
-def _workspace(where, ws, device):
-    if ws.device != device:
-        _bad(4, where, f"workspace is on {ws.device}, expected {device}")
+def _workspace(where, ws, dev):
+    if ws.get_device() != dev:
+        _bad(4, where, f"workspace is on {ws.device}, expected cuda:{dev}")
     if not ws.is_contiguous():
         _bad(2, where, "workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()

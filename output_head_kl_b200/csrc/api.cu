@@ -10,6 +10,7 @@
 // gradient G on chip, written once as bf16 into an N-independent chunk buffer,
 // and consumed by the dHidden and dW GEMMs before the next chunk overwrites it.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -122,9 +123,22 @@ bool make_map_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t out
 // --------------------------------------------------------------- planner
 kdkl_status current_device(Device& dv) {
   if (cudaGetDevice(&dv.id) != cudaSuccess) return fail(KDKL_ERR_UNSUPPORTED, "no CUDA device is current");
-  if (cudaDeviceGetAttribute(&dv.sms, cudaDevAttrMultiProcessorCount, dv.id) != cudaSuccess ||
-      cudaDeviceGetAttribute(&dv.cc_major, cudaDevAttrComputeCapabilityMajor, dv.id) != cudaSuccess)
-    return fail(KDKL_ERR_CUDA, "cudaDeviceGetAttribute failed");
+  // a device's properties do not change: looked up once per device (SM count and compute
+  // capability in one word, so that threads see both or neither)
+  static std::atomic<uint32_t> known[64];
+  const bool slot = dv.id >= 0 && dv.id < 64;
+  const uint32_t k = slot ? known[dv.id].load(std::memory_order_relaxed) : 0u;
+  if (k != 0) {
+    dv.sms = static_cast<int>(k & 0xFFFFu);
+    dv.cc_major = static_cast<int>(k >> 16);
+  } else {
+    if (cudaDeviceGetAttribute(&dv.sms, cudaDevAttrMultiProcessorCount, dv.id) != cudaSuccess ||
+        cudaDeviceGetAttribute(&dv.cc_major, cudaDevAttrComputeCapabilityMajor, dv.id) != cudaSuccess)
+      return fail(KDKL_ERR_CUDA, "cudaDeviceGetAttribute failed");
+    if (slot)
+      known[dv.id].store(static_cast<uint32_t>(dv.sms) | (static_cast<uint32_t>(dv.cc_major) << 16),
+                         std::memory_order_relaxed);
+  }
   if (dv.cc_major != 10) return fail(KDKL_ERR_UNSUPPORTED, "kdkl needs an sm_100 device (found cc %d.x)", dv.cc_major);
   return KDKL_OK;
 }

@@ -15,6 +15,12 @@ namespace {
 
 constexpr int32_t kMaxWidth = 1 << 20;
 constexpr size_t kFlagBytes = 256;
+// Shares of split tiles that a launch of large tiles may have (a wave of CTA pairs has 74 on B200), their
+// partial sums (256 x 256 fp32 each at most) and the tickets of their tiles.
+constexpr int kMaxShares = 80;
+constexpr int kMaxTailSplits = 8;
+constexpr size_t kShareBytes = 256 * 256 * 4;
+constexpr size_t kTicketBytes = kMaxShares / 2 * kTileTickets * 4;
 
 bool float_dtype(int32_t t) { return t == KDKL_BF16 || t == KDKL_F32; }
 
@@ -38,17 +44,28 @@ size_t norm_part_bytes(int64_t N, int32_t d) {
 struct Plan {
   bool pair = true;
   int tile = 256;    // pair: columns of a tile; small: rows of a tile
-  int splits = 1;
-  int code() const { return pair ? tile : splits * 1000 + tile; }
+  int splits = 1;    // pair: shares of each tile of the last wave; small: CTAs of a cluster
+  int code() const { return pair ? tile + (splits > 1 ? 10000 * splits : 0) : splits * 1000 + tile; }
 };
+
+// Tiles of the last, partly filled wave of large tiles (0 when every wave is full).
+int64_t tail_tiles(int64_t tiles, int sms) { return tiles % (sms / 2); }
+
+// The most shares that each tile of the last wave can be split into: all shares run at once, and each
+// keeps at least four reduction blocks.
+int most_splits(int64_t tail, int k_blocks, int sms) {
+  if (tail == 0) return 1;
+  const int64_t units = std::min<int64_t>(sms / 2, kMaxShares);
+  const int64_t s = std::min<int64_t>({units / tail, k_blocks / 4, kMaxTailSplits});
+  return static_cast<int>(std::max<int64_t>(s, 1));
+}
 
 // Product out[rows, cols] with `k_blocks` reduction blocks.
 //
 // Cost model in SM cycles.  Pair tiles: waves of ceil(tiles / pairs) tiles, each k_blocks x (2 x BN)
-// cycles of MMA at the tile's measured efficiency, then the last epilogue.  Small tiles: the larger of the
-// operand bytes that the SMs and the memory can move and one CTA's own chain of loads, plus the join.
-// Whichever is cheaper runs; the constants come from timing every plan over M = 1 to 4096 (the table in
-// front of plan_linear).
+// cycles of MMA at the tile's measured efficiency, then the last epilogue; the last wave may be split.
+// Small tiles: the larger of the operand bytes that the SMs and the memory can move and one CTA's own
+// chain of loads, plus the join.
 Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
   Plan best;
   double lo = 1e300;
@@ -56,14 +73,21 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
   const int64_t rb = (rows + 255) / 256;
   for (int bn : {256, 192, 128}) {
     const int64_t tiles = rb * ((cols + bn - 1) / bn);
-    const int64_t waves = (tiles + pairs - 1) / pairs;
+    const int64_t tail = tail_tiles(tiles, sms);
     const double eff = bn == 256 ? 0.85 : (bn == 192 ? 0.78 : 0.68);
-    const double c = static_cast<double>(waves) * (k_blocks * 2.0 * bn / eff + 700.0) + 6000.0;
-    if (c < lo * 0.99) {
-      lo = c;
-      best.pair = true;
-      best.tile = bn;
-      best.splits = 1;
+    const double per_kb = 2.0 * bn / eff;
+    const int most = most_splits(tail, k_blocks, sms);
+    for (int sp = 1; sp <= most; ++sp) {
+      const double full = static_cast<double>(tiles / pairs) * (k_blocks * per_kb + 700.0);
+      const double last = tail == 0 ? 0.0 : std::ceil(static_cast<double>(k_blocks) / sp) * per_kb + 700.0;
+      const double join = sp > 1 ? 7000.0 + 1000.0 * sp : 0.0;
+      const double c = full + last + join + 10000.0 + 20.0 * bn;
+      if (c < lo * 0.99) {
+        lo = c;
+        best.pair = true;
+        best.tile = bn;
+        best.splits = sp;
+      }
     }
   }
   if (op == kLinDw) return best;
@@ -90,10 +114,13 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
 }
 
 // A plan code of the caller's; false when the product has no such plan.
-bool decode_plan(int32_t code, LinOp op, int k_blocks, Plan& p) {
-  if (code == 128 || code == 192 || code == 256) {
-    p = Plan{true, code, 1};
-    return true;
+bool decode_plan(int32_t code, LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms, Plan& p) {
+  const int bn = code % 10000;
+  if (code > 0 && (bn == 128 || bn == 192 || bn == 256)) {
+    const int sp = code / 10000;
+    p = Plan{true, bn, sp == 0 ? 1 : sp};
+    const int64_t tiles = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
+    return sp == 0 || (sp >= 2 && sp <= most_splits(tail_tiles(tiles, sms), k_blocks, sms));
   }
   if (op == kLinDw || code < 1000) return false;
   const int sp = code / 1000, nt = code % 1000;
@@ -129,13 +156,24 @@ kdkl_linear_options default_linear_options() {
 }
 
 struct LinearLayout {
-  size_t dz = 0, part = 0, total = 0;
+  size_t tickets = 0, shares = 0, dz = 0, part = 0, total = 0;
 };
 
-// Gradient workspace: the flag word, dz, and the partial column sums of the most blocks act_grad runs.
-LinearLayout linear_layout(int64_t M, int32_t d_out, bool backward) {
+// Bytes of the partial sums that a product out[rows, cols] may split its last wave into, whatever its tile
+// width (narrower tiles are more, but smaller).
+size_t share_bytes(int64_t rows, int64_t cols) {
+  const int64_t tiles = ((rows + 255) / 256) * ((cols + 255) / 256);
+  return static_cast<size_t>(std::min<int64_t>(kMaxShares, tiles * kMaxTailSplits)) * kShareBytes;
+}
+
+// Workspace: the flag word, the tickets and partial sums of split tiles; for the gradient also dz and the
+// partial column sums of the most blocks act_grad runs.
+LinearLayout linear_layout(int64_t M, int32_t d_in, int32_t d_out, bool backward) {
   LinearLayout L;
-  size_t off = kFlagBytes;
+  L.tickets = kFlagBytes;
+  L.shares = align_up(L.tickets + kTicketBytes, 256);
+  size_t off = L.shares + (backward ? std::max(share_bytes(M, d_in), share_bytes(d_out, d_in))
+                                    : share_bytes(M, d_out));
   if (backward) {
     L.dz = off;
     off = align_up(off + static_cast<size_t>(M) * d_out * 2, 256);
@@ -160,29 +198,39 @@ cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b
   p.N = static_cast<int>(cols);
   p.k_blocks = reduction_blocks(static_cast<int32_t>(len), f8);
   p.splits = plan.splits;
-  CUtensorMap tmA, tmB;
   bool made;
   if (plan.pair) {
+    PairMaps m;
     const int bn = plan.tile;
     if (f8)
-      made = make_map_u8(&tmA, a, len, rows, len, 128, kBM, sw) && make_map_u8(&tmB, b, len, cols, len, 128, bn / 2, sw);
+      made = make_map_u8(&m.a, a, len, rows, len, 128, kBM, sw) && make_map_u8(&m.b, b, len, cols, len, 128, bn / 2, sw);
     else if (op == kLinFwd)
-      made = make_map(&tmA, a, len, rows, len, 64, kBM, sw) && make_map(&tmB, b, len, cols, len, 64, bn / 2, sw);
+      made = make_map(&m.a, a, len, rows, len, 64, kBM, sw) && make_map(&m.b, b, len, cols, len, 64, bn / 2, sw);
     else if (op == kLinDx)
-      made = make_map(&tmA, a, len, rows, len, 64, kBM, sw) && make_map(&tmB, b, cols, len, cols, 64, 64, sw);
+      made = make_map(&m.a, a, len, rows, len, 64, kBM, sw) && make_map(&m.b, b, cols, len, cols, 64, 64, sw);
     else
-      made = make_map(&tmA, a, rows, len, rows, 64, 64, sw) && make_map(&tmB, b, cols, len, cols, 64, 64, sw);
-    CUtensorMap tmOut, tmPre;
-    made = made && make_map(&tmOut, p.out, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
-           make_map(&tmPre, p.pre ? p.pre : p.out, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+      made = make_map(&m.a, a, rows, len, rows, 64, 64, sw) && make_map(&m.b, b, cols, len, cols, 64, 64, sw);
+    const auto box = [&](CUtensorMap* map, const void* base) {
+      return make_map(map, base, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    made = made && box(&m.out, p.out);
     if (!made) return cudaErrorInvalidValue;
+    m.pre = m.res = m.out;
+    if ((p.pre && !box(&m.pre, p.pre)) || (p.residual && !box(&m.res, p.residual))) return cudaErrorInvalidValue;
     p.n_tiles = static_cast<int>((cols + bn - 1) / bn);
-    p.units = static_cast<int>((rows + 255) / 256) * p.n_tiles;
-    p.row_group = 8;
+    p.tiles = static_cast<int>((rows + 255) / 256) * p.n_tiles;
+    const int tail = plan.splits > 1 ? static_cast<int>(tail_tiles(p.tiles, sms)) : 0;
+    p.full_units = p.tiles - tail;
+    p.units = p.full_units + tail * plan.splits;
+    // When B (the weights, or x for dW) stays in L2, two row blocks at a time read A once while it is
+    // hot: 412 against 424 us for 16384 x 4096 x 4096 at a steady clock; a B beyond L2 is swept for
+    // eight row blocks at a time.
+    p.row_group = static_cast<double>(cols) * len * (f8 ? 1 : 2) <= 48e6 ? 2 : 8;
     const int groups = std::min(p.units, sms / 2);
-    return launch_linear_pair(op, bn, tmA, tmB, tmOut, tmPre, p, 2 * groups, s);
+    return launch_linear_pair(op, bn, m, p, 2 * groups, s);
   }
   // small tiles: the weights take the MMA's M side
+  CUtensorMap tmA, tmB;
   const int nt = plan.tile;
   if (f8)
     made = make_map_u8(&tmA, b, len, cols, len, 128, 128, sw) && make_map_u8(&tmB, a, len, rows, len, 128, nt, sw);
@@ -194,6 +242,7 @@ cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b
   return launch_linear_small(op, nt, tmA, tmB, p, s);
 }
 
+// The plan of a product: the planner's (code 0) or the caller's.
 kdkl_status pick_plan(int32_t code, LinOp op, int64_t rows, int64_t cols, int64_t len, int sms, const char* name,
                       Plan& plan) {
   const int kb = reduction_blocks(static_cast<int32_t>(std::min<int64_t>(len, INT_MAX / 2)), op == kLinFwdE4M3);
@@ -201,7 +250,7 @@ kdkl_status pick_plan(int32_t code, LinOp op, int64_t rows, int64_t cols, int64_
     plan = plan_linear(op, rows, cols, kb, sms);
     return KDKL_OK;
   }
-  if (!decode_plan(code, op, kb, plan)) return fail(KDKL_ERR_UNSUPPORTED, "%s=%d is no plan of this product", name, code);
+  if (!decode_plan(code, op, rows, cols, kb, sms, plan)) return fail(KDKL_ERR_UNSUPPORTED, "%s=%d is no plan of this product", name, code);
   const int64_t tiles = plan.pair ? 0 : ((cols + 127) / 128) * ((rows + plan.tile - 1) / plan.tile) * plan.splits;
   if (tiles > INT_MAX / 2) return fail(KDKL_ERR_UNSUPPORTED, "%s=%d has too many tiles", name, code);
   return KDKL_OK;
@@ -219,18 +268,17 @@ kdkl_status device_with_pairs(Device& dv) {
   return KDKL_OK;
 }
 
-// In the bounds-checking build the kernels' checks can fail at once, so the flag word is cleared ahead of
-// the launch; in the normal build the call's first kernel clears it (linear.cu, clear_flags).
-kdkl_status debug_clear(void* workspace, cudaStream_t s) {
-#ifdef KDKL_DEBUG
-  const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes, s);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-#else
-  (void)workspace;
-  (void)s;
-#endif
-  return KDKL_OK;
+// Clears the flag word and the tickets of split tiles ahead of the launches.
+kdkl_status clear_header(void* workspace, cudaStream_t s) {
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes + kTicketBytes, s);
+  return e == cudaSuccess ? KDKL_OK : cuda_fail(e, "cudaMemsetAsync");
 }
+
+#ifdef KDKL_DEBUG
+constexpr bool kClearAhead = true;    // the kernels' checks can fail at once
+#else
+constexpr bool kClearAhead = false;   // without split tiles the call's kernel clears the flag word itself
+#endif
 
 }  // namespace
 }  // namespace kdkl
@@ -313,9 +361,9 @@ kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gam
   p.eps = eps;
   p.h_f32 = h_dtype == KDKL_F32;
   p.gamma_f32 = gamma_dtype == KDKL_F32;
-  const int blocks = rmsnorm_grad_blocks(N, d, dv.sms);
   const cudaError_t e = timed(kTNormGrad, s, [&] {
-    const cudaError_t e1 = launch_rmsnorm_grad(p, dv.sms, s);
+    cudaError_t e1;
+    const int blocks = launch_rmsnorm_grad(p, dv.sms, s, &e1);
     return e1 != cudaSuccess ? e1 : launch_colsum(p.part, blocks, d, dgamma, s);
   });
   if (e != cudaSuccess) return cuda_fail(e, "RMS norm gradient launch");
@@ -328,7 +376,7 @@ void kdkl_linear_options_init(kdkl_linear_options* options) {
 
 size_t kdkl_linear_workspace_bytes(int64_t M, int32_t d_in, int32_t d_out, int32_t backward) {
   if (check_linear_shape(M, d_in, d_out, KDKL_BF16) != KDKL_OK) return 0;
-  return linear_layout(M, d_out, backward != 0).total;
+  return linear_layout(M, d_in, d_out, backward != 0).total;
 }
 
 kdkl_status kdkl_linear_plan(int64_t M, int32_t d_in, int32_t d_out, int32_t operands, int32_t product,
@@ -375,7 +423,7 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   if (!aligned(o.x_scale, 4) || !aligned(o.w_scale, 16))
     return fail(KDKL_ERR_ALIGN, "x_scale must be 4-byte and w_scale 16-byte aligned");
   if (!aligned(workspace, 256)) return fail(KDKL_ERR_ALIGN, "workspace must be 256-byte aligned");
-  const LinearLayout L = linear_layout(M, d_out, false);
+  const LinearLayout L = linear_layout(M, d_in, d_out, false);
   if (workspace_bytes < L.total) return fail(KDKL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
   Device dv;
   if ((st = device_with_pairs(dv)) != KDKL_OK) return st;
@@ -383,12 +431,9 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   Plan plan;
   if ((st = pick_plan(o.plan, op, M, d_out, d_in, dv.sms, "plan", plan)) != KDKL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M == 0) {
-    const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes, s);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-    return ok();
-  }
-  if ((st = debug_clear(workspace, s)) != KDKL_OK) return st;
+  const bool clear_ahead = kClearAhead || M == 0 || (plan.pair && plan.splits > 1);
+  if (clear_ahead && (st = clear_header(workspace, s)) != KDKL_OK) return st;
+  if (M == 0) return ok();
   LinParams p = {};
   p.bias = static_cast<const uint16_t*>(bias);
   p.residual = static_cast<const uint16_t*>(residual);
@@ -398,7 +443,9 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   p.pre = static_cast<uint16_t*>(pre);
   p.act = o.activation;
   p.flags = static_cast<uint32_t*>(workspace);
-  p.clear_flags = 1;
+  p.clear_flags = clear_ahead ? 0 : 1;
+  p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.tickets);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.shares);
   const cudaError_t e = timed(kTLinear, s, [&] { return run_product(op, plan, x, W, M, d_out, d_in, p, dv.sms, s); });
   if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return ok();
@@ -423,7 +470,7 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
     return fail(KDKL_ERR_ALIGN, "dy, pre, x, W, dx and dW must be 16-byte aligned");
   if (!aligned(dbias, 4)) return fail(KDKL_ERR_ALIGN, "dbias must be 4-byte aligned");
   if (!aligned(workspace, 256)) return fail(KDKL_ERR_ALIGN, "workspace must be 256-byte aligned");
-  const LinearLayout L = linear_layout(M, d_out, true);
+  const LinearLayout L = linear_layout(M, d_in, d_out, true);
   if (workspace_bytes < L.total) return fail(KDKL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
   Device dv;
   if ((st = device_with_pairs(dv)) != KDKL_OK) return st;
@@ -433,7 +480,7 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   if (dW && (st = pick_plan(o.dw_plan, kLinDw, d_out, d_in, M, dv.sms, "dw_plan", dw_plan)) != KDKL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((e = cudaMemsetAsync(workspace, 0, kFlagBytes, s)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+  if ((st = clear_header(workspace, s)) != KDKL_OK) return st;
   if (M == 0) {
     if (dW && (e = cudaMemsetAsync(dW, 0, static_cast<size_t>(d_out) * d_in * 2, s)) != cudaSuccess)
       return cuda_fail(e, "cudaMemsetAsync");
@@ -457,6 +504,8 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   }
   LinParams p = {};
   p.flags = static_cast<uint32_t*>(workspace);
+  p.tickets = reinterpret_cast<uint32_t*>(ws + L.tickets);
+  p.part = reinterpret_cast<float*>(ws + L.shares);
   if (dx) {
     p.out = static_cast<uint16_t*>(dx);
     e = timed(kTLinearDx, s, [&] { return run_product(kLinDx, dx_plan, dz, W, M, d_in, d_out, p, dv.sms, s); });

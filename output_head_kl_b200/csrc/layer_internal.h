@@ -14,7 +14,7 @@ constexpr int kNormVec = 8;
 constexpr int kNormMaxThreads = 512;
 constexpr int kNormMaxD = kNormMaxThreads * kNormVec * 8;   // 8 steps of kNormVec elements per thread
 // Blocks of the gradient kernel, each leaving one row of partial sums for dgamma.
-constexpr int kNormGradBlocks = 592;
+constexpr int kNormGradBlocks = 1184;
 
 struct NormParams {
   const void* x;
@@ -42,9 +42,8 @@ struct NormGradParams {
   float eps;
   bool h_f32, gamma_f32;
 };
-// Blocks (rows of `part`) that launch_rmsnorm_grad uses.
-int rmsnorm_grad_blocks(int64_t N, int d, int sms);
-cudaError_t launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s);
+// Returns the blocks (rows of `part`) it used; *err is its launch's status.
+int launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s, cudaError_t* err);
 
 // out[c] = sum over rows of part[rows, n], in a fixed order.
 cudaError_t launch_colsum(const float* part, int rows, int n, float* out, cudaStream_t s);
@@ -61,10 +60,14 @@ struct LinParams {
   int M;                 // rows of the output
   int N;                 // columns of the output
   int k_blocks;          // 128-byte reduction blocks (dz and x as MN-major operands: 64 rows)
-  int units;             // output tiles
-  int n_tiles;           // tiles along N
-  int row_group;         // row blocks swept together (large tiles)
-  int splits;            // reduction splits = cluster size (small tiles)
+  int tiles;             // large tiles: output tiles, of which
+  int full_units;        //   the first full_units are computed whole and the others in `splits` shares;
+  int units;             //   units of work in all
+  int n_tiles;           //   tiles along N
+  int row_group;         //   row blocks swept together
+  int splits;            // shares of the reduction (small tiles: the cluster size)
+  float* part;           // large tiles: [shares][256 x bn] partial sums
+  uint32_t* tickets;     //   [split tiles][16] arrivals, zero before the launch and after it
   const uint16_t* bias;      // [N] bf16 or null
   const uint16_t* residual;  // [M, N] bf16 or null
   const float* x_scale;      // [M] or null
@@ -76,10 +79,13 @@ struct LinParams {
   int clear_flags;       // the first block zeroes the flag word
 };
 
+constexpr int kTileTickets = 16;   // epilogue warps of a CTA pair
 // Large tiles: 256 x bn (bn = 256, 192 or 128) by CTA pairs, persistent.
-cudaError_t launch_linear_pair(int op, int bn, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                               const CUtensorMap& tmOut, const CUtensorMap& tmPre, const LinParams& p, int grid,
-                               cudaStream_t s);
+struct PairMaps {
+  CUtensorMap a, b;           // operands
+  CUtensorMap out, pre, res;  // 32 x 32 boxes of y, z and the residual (unused ones repeat `out`)
+};
+cudaError_t launch_linear_pair(int op, int bn, const PairMaps& m, const LinParams& p, int grid, cudaStream_t s);
 // Small tiles: 128 output columns x nt rows (nt = 16, 32, 64 or 128) per cluster of p.splits CTAs; the
 // roles of the operands are swapped (tmA reads W, tmB reads x or dz).  op: all but kLinDw.
 cudaError_t launch_linear_small(int op, int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,

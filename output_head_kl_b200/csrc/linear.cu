@@ -129,6 +129,42 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Cluster barrier that orders execution only: nothing this thread wrote is waited for.  It closes the
+// kernels, where peers must not exit while their shared memory or TMEM is still in use.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// A 16-byte read that leaves L1 alone (read once).
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Brings a box of a tensor into L2.
+__device__ __forceinline__ void tma_prefetch_l2(const CUtensorMap* m, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
+// Arrival on a barrier of either CTA of the pair that says "this TMEM buffer has been read": the
+// tcgen05 fence before it orders the reads, so no cluster-wide release of other memory is waited for.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4u(uint32_t saddr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(saddr)
+               : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float4 ld_cluster_v4f(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -149,9 +185,7 @@ struct LinLayout {
 // Zeroes the flag word before any of this launch's waits can time out (they take kWaitLimitNs at
 // least; the bounds-checking build, whose checks can fail at once, clears it ahead of the launch).
 __device__ __forceinline__ void clear_flags(const LinParams& p) {
-#ifndef KDKL_DEBUG
   if (p.clear_flags && blockIdx.x == 0 && threadIdx.x == 0) *p.flags = 0u;
-#endif
 }
 
 // ============================================================================
@@ -175,8 +209,12 @@ struct PairCfg {
   static constexpr int kBBytes = kBmn ? kBAtoms * 8192 : kCtaN * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kTxBytes = 2 * kStageBytes;          // both CTAs' bytes, counted on the even CTA
-  static constexpr int kEpiWarpBytes = 2 * 2048;            // two 32 x 32 bf16 staging buffers
-  static constexpr int kEpiBytes = kEpiWarps * kEpiWarpBytes;
+  // per epilogue warp: two 32 x 32 bf16 staging buffers for stores and, with the full epilogue, one for the
+  // residual and the bias and scales of the warp's BN / 2 columns
+  static constexpr int kStageBuf = 2048;
+  static constexpr int kSideBytes = L::kFull ? (BN / 2) * 4 * (L::kF8 ? 2 : 1) : 0;
+  static constexpr int kEpiWarpBytes = (L::kFull ? 3 : 2) * kStageBuf + kSideBytes;
+  static constexpr int kEpiBytes = (kEpiWarps * kEpiWarpBytes + 1023) / 1024 * 1024;
   static constexpr int kStagesFit = (232448 - 1024 - kEpiBytes - 512) / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + 512;
@@ -184,24 +222,45 @@ struct PairCfg {
   static constexpr int kAccStride = BN <= 128 ? 128 : 256;
   static constexpr uint32_t kTmemCols = 2 * kAccStride;
   static_assert(BN % 64 == 0 && BN >= 128 && BN <= 256, "two halves of whole 32-column chunks");
-  static_assert(kStages >= 4 && (2 * kStages + 5) * 8 + 16 <= 512, "stages");
+  static_assert(kStages >= 4 && (2 * kStages + 5 + kEpiWarps) * 8 + 16 <= 512, "stages");
 };
 
-__device__ __forceinline__ void lin_tile(const LinParams& p, int u, int& mb, int& t) {
-  const int rows = p.units / p.n_tiles;
-  const int g = u / (p.row_group * p.n_tiles);
-  const int r0 = g * p.row_group;
+// Unit u: an output tile (row block mb, column tile t) and its reduction blocks [kb0, kb1).  The units from
+// full_units on are the last, partly filled wave's tiles, each split into `splits` shares of the reduction;
+// `share` counts them over all those tiles (-1 for a whole tile).
+struct PairUnit {
+  int mb, t, kb0, kb1, share;
+};
+
+__device__ __forceinline__ PairUnit pair_unit(const LinParams& p, int u) {
+  PairUnit w;
+  int tile = u;
+  w.kb0 = 0;
+  w.kb1 = p.k_blocks;
+  w.share = -1;
+  if (u >= p.full_units) {
+    const int tail = p.tiles - p.full_units;
+    const int s = (u - p.full_units) / tail, i = u - p.full_units - s * tail;
+    tile = p.full_units + i;
+    w.kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * s / p.splits);
+    w.kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (s + 1) / p.splits);
+    w.share = i * p.splits + s;
+  }
+  // groups of row_group row blocks, each swept column by column
+  const int rows = p.tiles / p.n_tiles;
+  const int r0 = tile / (p.row_group * p.n_tiles) * p.row_group;
   const int rg = min(p.row_group, rows - r0);
-  const int off = u - r0 * p.n_tiles;
-  t = off / rg;
-  mb = r0 + off - t * rg;
+  const int off = tile - r0 * p.n_tiles;
+  w.t = off / rg;
+  w.mb = r0 + off - w.t * rg;
+  return w;
 }
 
 template <int OP, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre,
-                       const LinParams p) {
+                       const __grid_constant__ CUtensorMap tmRes, const LinParams p) {
   using C = PairCfg<OP, BN>;
   using L = LinLayout<OP>;
   extern __shared__ uint8_t smem_raw[];
@@ -214,7 +273,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* res_full = drain + 1;   // one per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,6 +282,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int group = static_cast<int>(blockIdx.x >> 1), ngroups = static_cast<int>(gridDim.x >> 1);
 
   clear_flags(p);
+  if (threadIdx.x == 64) {   // the descriptors travel while the barriers are set up
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
+    if (L::kFull && p.pre) tma_prefetch_desc(&tmPre);
+    if (L::kFull && p.residual) tma_prefetch_desc(&tmRes);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -232,11 +299,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&res_full[w], 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmOut);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, C::kTmemCols);
@@ -255,11 +320,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       uint32_t phase = 0;
       bool wrapped = false, stop = false;
       for (int u = group; u < p.units && !stop; u += ngroups) {
-        int mb, t;
-        lin_tile(p, u, mb, t);
-        const int arow = mb * 256 + static_cast<int>(rank) * kBM;
-        const int brow = t * BN + static_cast<int>(rank) * C::kCtaN;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        const PairUnit w = pair_unit(p, u);
+        const int arow = w.mb * 256 + static_cast<int>(rank) * kBM;
+        const int brow = w.t * BN + static_cast<int>(rank) * C::kCtaN;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, ab)) {
             stop = true;
             break;
@@ -310,7 +374,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::kAccStride);
         bool got = true;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        const PairUnit w = pair_unit(p, u);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           got = mbar_wait(&full[stage], phase, ab);
           if (!got) break;
           tc_fence_after();
@@ -322,7 +387,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                         : sdesc_sw128(a_addr + j * 32, 16, 1024);
             const uint64_t bd = C::kBmn ? sdesc_sw128(b_addr + j * 2048, 8192, 1024)
                                         : sdesc_sw128(b_addr + j * 32, 16, 1024);
-            umma<L::kF8, true>(d_tmem, ad, bd, C::kIdesc, (kb | j) != 0 ? 1u : 0u);
+            umma<L::kF8, true>(d_tmem, ad, bd, C::kIdesc, (kb != w.kb0 || j != 0) ? 1u : 0u);
           }
           umma_commit_pair(&empty[stage], 0x3);
           if (++stage == C::kStages) {
@@ -351,9 +416,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lane_addr = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t acc_empty0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
-    uint8_t* wbuf = sEpi + (warp - 2) * C::kEpiWarpBytes;
+    // staging buffers (2 KB each, so that the 64-byte swizzle starts over in each): stores, then residual
+    uint8_t* wbuf = sEpi + (warp - 2) * (L::kFull ? 3 : 2) * C::kStageBuf;
+    uint8_t* rbuf = wbuf + 2 * C::kStageBuf;
+    const uint32_t side = smem_u32(sEpi + kEpiWarps * (L::kFull ? 3 : 2) * C::kStageBuf + (warp - 2) * C::kSideBytes);
     int sbuf = 0, acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t acc_phase = 0, res_phase = 0;
+    bool res_pending = false;
+    auto load_res = [&](int col, int row) {   // one lane; rows past M and columns past N arrive as zero
+      mbar_arrive_expect_tx(&res_full[warp - 2], C::kStageBuf);
+      tma_load_2d(rbuf, &tmRes, &res_full[warp - 2], dbg_ok((col & 7) == 0, p.flags) ? col : (col & ~7), row);
+    };
     // stages 32 rows x 32 bf16 columns (64-byte swizzle) and stores them by TMA, which clips the
     // columns past N and the rows past M
     auto store32 = [&](const CUtensorMap* tm, const float(&v)[32], int col, int row) {
@@ -376,80 +449,170 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       sbuf ^= 1;
     };
     for (int u = group; u < p.units; u += ngroups) {
-      int mb, t;
-      lin_tile(p, u, mb, t);
-      const int row0 = mb * 256 + static_cast<int>(rank) * kBM + q * 32;   // the warp's first row
+      const PairUnit w = pair_unit(p, u);
+      const bool split = w.share >= 0;
+      const int row0 = w.mb * 256 + static_cast<int>(rank) * kBM + q * 32;   // the warp's first row
       const int row = row0 + lane;
-      const int c_first = t * BN + half * (BN / 2);
-      uint4 res[4];
+      const int c_first = w.t * BN + half * (BN / 2);
+      // What the epilogue reads is fetched while the tile's MMAs run: the residual's first 32-column chunk
+      // into shared memory and the others into L2, bias and scales as fp32 into shared memory.
       float xs = 1.f;
-      const bool has_res = L::kFull && p.residual != nullptr && row < p.M;
-      auto load_res = [&](int col) {
-        const uint16_t* src = p.residual + static_cast<int64_t>(row) * p.N + col;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (col + g * 8 < p.N) res[g] = *reinterpret_cast<const uint4*>(src + g * 8);
-      };
       if (L::kFull) {
-        // fetched while the tile's MMAs run
+        if (!split && p.residual && lane == 0 && c_first < p.N) {
+          load_res(c_first, row0);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) res[g] = make_uint4(0u, 0u, 0u, 0u);
-        if (has_res && c_first < p.N) load_res(c_first);
+          for (int c = 1; c < BN / 64; ++c)
+            if (c_first + c * 32 < p.N) tma_prefetch_l2(&tmRes, c_first + c * 32, row0);
+        }
+        res_pending = !split && p.residual != nullptr && c_first < p.N;
+        __syncwarp();   // every lane has read the last tile's bias and scales
+        const int lc = lane * 4;
+        if (lc < BN / 2 && c_first + lc < p.N) {
+          if (p.bias) {
+            const uint2 b = *reinterpret_cast<const uint2*>(p.bias + c_first + lc);
+            st_shared_v4(side + lc * 4, __float_as_uint(bf_lo(b.x)), __float_as_uint(bf_hi(b.x)),
+                         __float_as_uint(bf_lo(b.y)), __float_as_uint(bf_hi(b.y)));
+          }
+          if (L::kF8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p.w_scale + c_first + lc);
+            st_shared_v4(side + (BN / 2) * 4 + lc * 4, w.x, w.y, w.z, w.w);
+          }
+        }
         if (L::kF8 && row < p.M) xs = p.x_scale[row];
+        __syncwarp();
       }
       if (!mbar_wait(&acc_full[acc], acc_phase, ab)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + lane_addr + static_cast<uint32_t>(acc * C::kAccStride + half * (BN / 2));
+      auto release_acc = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(acc_empty0 + static_cast<uint32_t>(acc) * 8u);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      };
+      // A share of a split tile: the warp leaves its partial sums in the workspace (as groups of four columns,
+      // lane by lane) and takes a ticket; the warp with the last one adds the shares up in their order
+      // and finishes the tile, so the result does not depend on which that is.
+      const int64_t warp_floats = 32 * (BN / 2);
+      const int wslot = static_cast<int>(rank) * kEpiWarps + (warp - 2);
+      float4* mine = reinterpret_cast<float4*>(
+          p.part + (static_cast<int64_t>(w.share) * (2 * kEpiWarps) + wslot) * warp_floats);
+      if (split) {
+#pragma unroll 1
+        for (int c = 0; c < BN / 64; ++c) {
+          if (c_first + c * 32 >= p.N) break;
+          float v[32];
+          tmem_ld32(tbase + c * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            __stcg(mine + (c * 8 + g) * 32 + lane, make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]));
+        }
+        release_acc();
+        __threadfence();
+        __syncwarp();
+        uint32_t* ticket = p.tickets + w.share / p.splits * (2 * kEpiWarps) + wslot;
+        int last = 0;
+        if (lane == 0) {
+          last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(p.splits - 1);
+          if (last) *ticket = 0u;   // as the next launch finds it
+        }
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        __threadfence();
+        if (L::kFull && p.residual && c_first < p.N) {
+          res_pending = true;
+          if (lane == 0) load_res(c_first, row0);
+        }
+      }
+      const float4* shares = reinterpret_cast<const float4*>(
+          p.part + (static_cast<int64_t>(split ? w.share / p.splits * p.splits : 0) * (2 * kEpiWarps) + wslot) *
+                       warp_floats);
+      bool got = true;
 #pragma unroll 1
       for (int c = 0; c < BN / 64; ++c) {
         const int col = c_first + c * 32;
         if (col >= p.N) break;
         float v[32];
-        tmem_ld32(tbase + c * 32, v);
-        tmem_wait_ld();
+        if (!split) {
+          tmem_ld32(tbase + c * 32, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll 1
+          for (int s2 = 0; s2 < p.splits; s2 += 2) {   // two shares' loads in flight, added in order
+            const int64_t share_f4 = (2 * kEpiWarps) * (warp_floats / 4);
+            const float4* from = shares + s2 * share_f4 + c * 256 + lane;
+            const bool two = s2 + 1 < p.splits;
+            float4 o[2][8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) o[0][g] = __ldcg(from + g * 32);
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              o[1][g] = two ? __ldcg(from + share_f4 + g * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              v[g * 4 + 0] = (v[g * 4 + 0] + o[0][g].x) + o[1][g].x;
+              v[g * 4 + 1] = (v[g * 4 + 1] + o[0][g].y) + o[1][g].y;
+              v[g * 4 + 2] = (v[g * 4 + 2] + o[0][g].z) + o[1][g].z;
+              v[g * 4 + 3] = (v[g * 4 + 3] + o[0][g].w) + o[1][g].w;
+            }
+          }
+        }
         if (L::kFull) {
           if (L::kF8) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-              if (col + g * 4 < p.N) {
-                const float4 w = *reinterpret_cast<const float4*>(p.w_scale + col + g * 4);
-                v[g * 4 + 0] *= xs * w.x;
-                v[g * 4 + 1] *= xs * w.y;
-                v[g * 4 + 2] *= xs * w.z;
-                v[g * 4 + 3] *= xs * w.w;
-              }
+            for (int g = 0; g < 8; ++g) {
+              const float4 w = ld_shared_v4f(side + (BN / 2) * 4 + (c * 32 + g * 4) * 4);
+              v[g * 4 + 0] *= xs * w.x;
+              v[g * 4 + 1] *= xs * w.y;
+              v[g * 4 + 2] *= xs * w.z;
+              v[g * 4 + 3] *= xs * w.w;
+            }
           }
           if (p.bias) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (col + g * 8 < p.N) {
-                const uint4 b = *reinterpret_cast<const uint4*>(p.bias + col + g * 8);
-                v[g * 8 + 0] += bf_lo(b.x), v[g * 8 + 1] += bf_hi(b.x);
-                v[g * 8 + 2] += bf_lo(b.y), v[g * 8 + 3] += bf_hi(b.y);
-                v[g * 8 + 4] += bf_lo(b.z), v[g * 8 + 5] += bf_hi(b.z);
-                v[g * 8 + 6] += bf_lo(b.w), v[g * 8 + 7] += bf_hi(b.w);
-              }
+            for (int g = 0; g < 8; ++g) {
+              const float4 b = ld_shared_v4f(side + (c * 32 + g * 4) * 4);
+              v[g * 4 + 0] += b.x;
+              v[g * 4 + 1] += b.y;
+              v[g * 4 + 2] += b.z;
+              v[g * 4 + 3] += b.w;
+            }
           }
           if (p.pre) store32(&tmPre, v, col, row0);
           act_all(v, p.act);
           if (p.residual) {
+            got = mbar_wait(&res_full[warp - 2], res_phase, ab);
+            if (!got) break;
+            res_phase ^= 1u;
+            const uint32_t addr = smem_u32(rbuf) + static_cast<uint32_t>(lane) * 64u;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              v[g * 8 + 0] += bf_lo(res[g].x), v[g * 8 + 1] += bf_hi(res[g].x);
-              v[g * 8 + 2] += bf_lo(res[g].y), v[g * 8 + 3] += bf_hi(res[g].y);
-              v[g * 8 + 4] += bf_lo(res[g].z), v[g * 8 + 5] += bf_hi(res[g].z);
-              v[g * 8 + 6] += bf_lo(res[g].w), v[g * 8 + 7] += bf_hi(res[g].w);
+              const uint4 r = ld_shared_v4u(addr + ((static_cast<uint32_t>(g) ^ ((lane >> 1) & 3u)) << 4));
+              v[g * 8 + 0] += bf_lo(r.x), v[g * 8 + 1] += bf_hi(r.x);
+              v[g * 8 + 2] += bf_lo(r.y), v[g * 8 + 3] += bf_hi(r.y);
+              v[g * 8 + 4] += bf_lo(r.z), v[g * 8 + 5] += bf_hi(r.z);
+              v[g * 8 + 6] += bf_lo(r.w), v[g * 8 + 7] += bf_hi(r.w);
             }
-            if (has_res && c + 1 < BN / 64 && col + 32 < p.N) load_res(col + 32);
+            // The next chunk's load may overwrite the buffer only after every lane has its values: the sums
+            // above have used them (a read that is merely issued is not ordered before a TMA write).
+            __syncwarp();
+            res_pending = c + 1 < BN / 64 && col + 32 < p.N;
+            if (res_pending && lane == 0) load_res(col + 32, row0);
           }
         }
         store32(&tmOut, v, col, row0);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty0 + static_cast<uint32_t>(acc) * 8u);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      if (!got) break;
+      if (!split) release_acc();
+    }
+    if (res_pending && lane == 0) {
+      // giving up with a residual chunk on its way: bounded wait
+      const uint64_t w0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&res_full[warp - 2]), res_phase) && globaltimer_ns() - w0 < kDrainLimitNs) {
+      }
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
@@ -462,7 +625,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   }
   tc_fence_before();
-  cluster_sync();   // the peer's shared memory and TMEM stay alive until the pair is done
+  cluster_sync_relaxed();   // the peer's shared memory and TMEM stay alive until the pair is done
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::kTmemCols);
@@ -478,6 +641,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // adds the partial sums in CTA order.  No workspace, no atomics, one launch.
 // ============================================================================
 constexpr int kSmallThreads = 192;
+constexpr int kMaxSplits = 8;
+constexpr int kBatch = 2;
 
 template <int OP, int NT>
 struct SmallCfg {
@@ -522,8 +687,21 @@ __global__ void __launch_bounds__(kSmallThreads)
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
 
-  clear_flags(p);
+  auto load = [&](int kb, int stage) {
+    uint8_t* a = sA + stage * C::kABytes;
+    mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+    if (C::kAmn) {
+      tma_load_2d(a, &tmA, &full[stage], col0, kb * 64);
+      tma_load_2d(a + 8192, &tmA, &full[stage], col0 + 64, kb * 64);
+    } else {
+      tma_load_2d(a, &tmA, &full[stage], kb * L::kStepElems, col0);
+    }
+    tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * L::kStepElems, row0);
+  };
   if (threadIdx.x == 0) {
+    // the loading thread sets up the barriers and fills the stages before it meets the others
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
@@ -531,6 +709,8 @@ __global__ void __launch_bounds__(kSmallThreads)
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    for (int s = 0; s < C::kStages && kb0 + s < kb1; ++s) load(kb0 + s, s);
+    clear_flags(p);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -542,21 +722,40 @@ __global__ void __launch_bounds__(kSmallThreads)
   const uint32_t tmem_base = *tmem_slot;
   const AbortState ab{abort_flag, p.flags};
 
+  // This CTA's share of the tile: items are groups of four columns of a row, kBatch of a thread at a time.
+  // What the first batch reads beside the product is fetched while the product runs.
+  const int rows = min(NT, p.M - row0);
+  const int items = rows * 32;
+  const int i0 = static_cast<int>(static_cast<int64_t>(items) * rank / p.splits);
+  const int i1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / p.splits);
+  struct Side {
+    uint2 res, bias;
+    float4 ws;
+    float xs;
+  };
+  auto load_side = [&](int i, Side& d) {
+    const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
+    d.res = d.bias = make_uint2(0u, 0u);
+    d.xs = 1.f;
+    if (!L::kFull || i >= i1 || col >= p.N) return;
+    if (p.residual) d.res = *reinterpret_cast<const uint2*>(p.residual + static_cast<int64_t>(row) * p.N + col);
+    if (p.bias) d.bias = *reinterpret_cast<const uint2*>(p.bias + col);
+    if (L::kF8) {
+      d.xs = p.x_scale[row];
+      d.ws = *reinterpret_cast<const float4*>(p.w_scale + col);
+    }
+  };
+  Side side[kBatch];
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) load_side(i0 + static_cast<int>(threadIdx.x) + b * kSmallThreads, side[b]);
+
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      uint32_t phase = 1;
+      for (int kb = kb0 + C::kStages; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, ab)) break;
-        uint8_t* a = sA + stage * C::kABytes;
-        mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
-        if (C::kAmn) {
-          tma_load_2d(a, &tmA, &full[stage], col0, kb * 64);
-          tma_load_2d(a + 8192, &tmA, &full[stage], col0 + 64, kb * 64);
-        } else {
-          tma_load_2d(a, &tmA, &full[stage], kb * L::kStepElems, col0);
-        }
-        tma_load_2d(sB + stage * C::kBBytes, &tmB, &full[stage], kb * L::kStepElems, row0);
+        load(kb, stage);
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
@@ -621,50 +820,56 @@ __global__ void __launch_bounds__(kSmallThreads)
     tmem_dealloc(tmem_base, C::kTmemCols);
   }
   if (good) {
-    const int rows = min(NT, p.M - row0);
-    const int items = rows * 32;                  // groups of four columns
-    const int i0 = static_cast<int>(static_cast<int64_t>(items) * rank / p.splits);
-    const int i1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / p.splits);
     const uint32_t base = smem_u32(part);
-    for (int i = i0 + static_cast<int>(threadIdx.x); i < i1; i += kSmallThreads) {
-      const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
-      if (col >= p.N) continue;
-      const int64_t at = static_cast<int64_t>(row) * p.N + col;
-      uint2 res = make_uint2(0u, 0u);
-      if (L::kFull && p.residual) res = *reinterpret_cast<const uint2*>(p.residual + at);
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < p.splits; ++s) {
-        const float4 q = ld_cluster_v4f(mapa_shared(base + static_cast<uint32_t>(i) * 16u, s));
-        v[0] += q.x;
-        v[1] += q.y;
-        v[2] += q.z;
-        v[3] += q.w;
+    for (int first = i0 + static_cast<int>(threadIdx.x); first < i1; first += kBatch * kSmallThreads) {
+      float4 q[kBatch][kMaxSplits];   // all partial sums of the batch are in flight before the first is added
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        // only what is used below is read: its use orders the reads before the closing barrier
+        const int i = first + b * kSmallThreads;
+        const bool live = i < i1 && col0 + (i & 31) * 4 < p.N;
+#pragma unroll
+        for (int s = 0; s < kMaxSplits; ++s)
+          if (s < p.splits && live)
+            q[b][s] = ld_cluster_v4f(mapa_shared(base + static_cast<uint32_t>(i) * 16u, s));
       }
-      if (L::kFull) {
-        if (L::kF8) {
-          const float xs = p.x_scale[row];
-          const float4 w = *reinterpret_cast<const float4*>(p.w_scale + col);
-          v[0] *= xs * w.x;
-          v[1] *= xs * w.y;
-          v[2] *= xs * w.z;
-          v[3] *= xs * w.w;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = first + b * kSmallThreads;
+        const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
+        if (i >= i1 || col >= p.N) continue;
+        const int64_t at = static_cast<int64_t>(row) * p.N + col;
+        float v[4] = {q[b][0].x, q[b][0].y, q[b][0].z, q[b][0].w};
+#pragma unroll
+        for (int s = 1; s < kMaxSplits; ++s)
+          if (s < p.splits) {
+            v[0] += q[b][s].x;
+            v[1] += q[b][s].y;
+            v[2] += q[b][s].z;
+            v[3] += q[b][s].w;
+          }
+        if (L::kFull) {
+          const Side& d = side[b];
+          if (L::kF8) {
+            v[0] *= d.xs * d.ws.x;
+            v[1] *= d.xs * d.ws.y;
+            v[2] *= d.xs * d.ws.z;
+            v[3] *= d.xs * d.ws.w;
+          }
+          if (p.bias) v[0] += bf_lo(d.bias.x), v[1] += bf_hi(d.bias.x), v[2] += bf_lo(d.bias.y), v[3] += bf_hi(d.bias.y);
+          if (p.pre)
+            *reinterpret_cast<uint2*>(p.pre + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          act_all(v, p.act);
+          if (p.residual) v[0] += bf_lo(d.res.x), v[1] += bf_hi(d.res.x), v[2] += bf_lo(d.res.y), v[3] += bf_hi(d.res.y);
         }
-        if (p.bias) {
-          const uint2 b = *reinterpret_cast<const uint2*>(p.bias + col);
-          v[0] += bf_lo(b.x), v[1] += bf_hi(b.x), v[2] += bf_lo(b.y), v[3] += bf_hi(b.y);
-        }
-        if (p.pre)
-          *reinterpret_cast<uint2*>(p.pre + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        act_all(v, p.act);
-        if (p.residual) {
-          v[0] += bf_lo(res.x), v[1] += bf_hi(res.x), v[2] += bf_lo(res.y), v[3] += bf_hi(res.y);
-        }
+        *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
       }
-      *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) load_side(first + (kBatch + b) * kSmallThreads, side[b]);
     }
   }
   __syncwarp();
-  cluster_sync();   // this CTA's partial tile stays readable until every peer has joined its share
+  cluster_sync_relaxed();   // this CTA's partial tile stays readable until every peer has joined its share
 }
 
 // ============================================================================
@@ -685,23 +890,36 @@ __global__ void __launch_bounds__(32 * kActRows)
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   if (col < n) {
-#pragma unroll 4
-    for (int64_t r = r0 + threadIdx.y; r < r1; r += kActRows) {
-      const int64_t at = r * n + col;
-      const uint4 g = *reinterpret_cast<const uint4*>(dy + at);
-      float v[8] = {bf_lo(g.x), bf_hi(g.x), bf_lo(g.y), bf_hi(g.y), bf_lo(g.z), bf_hi(g.z), bf_lo(g.w), bf_hi(g.w)};
-      if (ACT != KDKL_ACT_NONE) {
-        const uint4 z = *reinterpret_cast<const uint4*>(pre + at);
-        const float w[8] = {bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y),
-                            bf_lo(z.z), bf_hi(z.z), bf_lo(z.w), bf_hi(z.w)};
+    constexpr int kU = 4;   // rows whose loads are in flight together
+    int64_t r = r0 + threadIdx.y;
+    for (; r < r1; r += kU * kActRows) {
+      uint4 g[kU], z[kU];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(w[j]);
-        if (dz)
-          *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                          pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      for (int u = 0; u < kU; ++u) {
+        const int64_t at = (r + u * kActRows) * n + col;
+        if (r + u * kActRows < r1) {
+          g[u] = ld_stream16(dy + at);
+          if (ACT != KDKL_ACT_NONE) z[u] = ld_stream16(pre + at);
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      for (int u = 0; u < kU; ++u) {
+        if (r + u * kActRows >= r1) break;
+        float v[8] = {bf_lo(g[u].x), bf_hi(g[u].x), bf_lo(g[u].y), bf_hi(g[u].y),
+                      bf_lo(g[u].z), bf_hi(g[u].z), bf_lo(g[u].w), bf_hi(g[u].w)};
+        if (ACT != KDKL_ACT_NONE) {
+          const float w[8] = {bf_lo(z[u].x), bf_hi(z[u].x), bf_lo(z[u].y), bf_hi(z[u].y),
+                              bf_lo(z[u].z), bf_hi(z[u].z), bf_lo(z[u].w), bf_hi(z[u].w)};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= act_grad_f<ACT>(w[j]);
+          if (dz)
+            *reinterpret_cast<uint4*>(dz + (r + u * kActRows) * n + col) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                           pack_bf16x2(v[6], v[7]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      }
     }
   }
   if (!part) return;
@@ -749,24 +967,22 @@ cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, int smem, uns
 }
 
 template <int OP, int BN>
-cudaError_t pair_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
-                     const CUtensorMap& tmPre, const LinParams& p, int grid, cudaStream_t s) {
+cudaError_t pair_one(const PairMaps& m, const LinParams& p, int grid, cudaStream_t s) {
   using C = PairCfg<OP, BN>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = configure(linear_pair_kernel<OP, BN>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = cluster_config(static_cast<unsigned>(grid), kPairThreads, C::kSmem, 2, s, &attr);
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OP, BN>, tmA, tmB, tmOut, tmPre, p);
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OP, BN>, m.a, m.b, m.out, m.pre, m.res, p);
 }
 
 template <int OP>
-cudaError_t pair_op(int bn, const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmOut,
-                    const CUtensorMap& tmPre, const LinParams& p, int grid, cudaStream_t s) {
+cudaError_t pair_op(int bn, const PairMaps& m, const LinParams& p, int grid, cudaStream_t s) {
   switch (bn) {
-    case 256: return pair_one<OP, 256>(tmA, tmB, tmOut, tmPre, p, grid, s);
-    case 192: return pair_one<OP, 192>(tmA, tmB, tmOut, tmPre, p, grid, s);
-    case 128: return pair_one<OP, 128>(tmA, tmB, tmOut, tmPre, p, grid, s);
+    case 256: return pair_one<OP, 256>(m, p, grid, s);
+    case 192: return pair_one<OP, 192>(m, p, grid, s);
+    case 128: return pair_one<OP, 128>(m, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -797,14 +1013,12 @@ cudaError_t small_op(int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, con
 
 }  // namespace
 
-cudaError_t launch_linear_pair(int op, int bn, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                               const CUtensorMap& tmOut, const CUtensorMap& tmPre, const LinParams& p, int grid,
-                               cudaStream_t s) {
+cudaError_t launch_linear_pair(int op, int bn, const PairMaps& m, const LinParams& p, int grid, cudaStream_t s) {
   switch (op) {
-    case kLinFwd: return pair_op<kLinFwd>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
-    case kLinFwdE4M3: return pair_op<kLinFwdE4M3>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
-    case kLinDx: return pair_op<kLinDx>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
-    case kLinDw: return pair_op<kLinDw>(bn, tmA, tmB, tmOut, tmPre, p, grid, s);
+    case kLinFwd: return pair_op<kLinFwd>(bn, m, p, grid, s);
+    case kLinFwdE4M3: return pair_op<kLinFwdE4M3>(bn, m, p, grid, s);
+    case kLinDx: return pair_op<kLinDx>(bn, m, p, grid, s);
+    case kLinDw: return pair_op<kLinDw>(bn, m, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
 }

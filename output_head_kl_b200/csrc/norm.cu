@@ -8,6 +8,7 @@
 // Both are bound by HBM: every element is read once and written once, a row stays in registers
 // between the statistics and the output, and all sums are held in fp32.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "kdkl_internal.h"
@@ -32,6 +33,7 @@ struct Pack<false> {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
   }
+  __device__ __forceinline__ void load_pieces(const void* p, const void*) { a = *static_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&v)[kV]) const {
     v[0] = bf_lo(a.x), v[1] = bf_hi(a.x), v[2] = bf_lo(a.y), v[3] = bf_hi(a.y);
@@ -50,6 +52,10 @@ struct Pack<true> {
     const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     a = q[0];
     b = q[1];
+  }
+  __device__ __forceinline__ void load_pieces(const void* p, const void* q) {
+    a = *static_cast<const float4*>(p);
+    b = *static_cast<const float4*>(q);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[kV]) const {
@@ -102,7 +108,14 @@ __device__ __forceinline__ float row_reduce(float v, float* slot, int warps) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) slot[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < warps ? slot[lane] : 0.f;   // every warp reduces the same values in the same order
+  // every thread reduces the same values in the same order: reading them is cheapest for a few warps, another
+  // round of shuffles the shorter chain for many (2.1 against 2.4 us for one row of 4096)
+  if (warps <= 8) {
+    v = slot[0];
+    for (int w = 1; w < warps; ++w) v = MAX ? max_nan(v, slot[w]) : v + slot[w];
+    return v;
+  }
+  v = lane < warps ? slot[lane] : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
@@ -162,7 +175,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
     }
   }
   ss = row_reduce<WARP, false>(ss, s_red[0], warps);
-  const float r = 1.0f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
+  const float r = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -179,11 +192,16 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
   if (Q) {
     top = row_reduce<WARP, true>(top, s_red[1], warps);
     if (lane_t == 0) p.y_scale[n] = top / kE4m3Max;
-    // q = y * (448 / top); a row of zeros has scale 0 and q = 0, and a row so small that 448 / top
-    // would overflow is divided by its scale instead
-    const bool tiny = top < 1e-30f;
-    const float inv = tiny ? 0.f : kE4m3Max / top;
-    const float scale = top / kE4m3Max;
+    // q = y * (448 / top); a row of zeros has scale 0 and q = 0, and a row so small that 448 / top would
+    // overflow is first multiplied by a power of two, which is exact
+    if (top < 1e-30f) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[i][j] *= 0x1p100f;
+      top *= 0x1p100f;
+    }
+    const float inv = top == 0.f ? 0.f : kE4m3Max / top;
     uint8_t* out = static_cast<uint8_t*>(p.y);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -191,7 +209,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
       if (c < p.d) {
         float q[kV];
 #pragma unroll
-        for (int j = 0; j < kV; ++j) q[j] = !tiny ? v[i][j] * inv : (scale > 0.f ? v[i][j] / scale : 0.f);
+        for (int j = 0; j < kV; ++j) q[j] = v[i][j] * inv;
         *reinterpret_cast<uint2*>(out + base + c) =
             make_uint2(pack_e4m3x2(q[0], q[1]) | (pack_e4m3x2(q[2], q[3]) << 16),
                        pack_e4m3x2(q[4], q[5]) | (pack_e4m3x2(q[6], q[7]) << 16));
@@ -200,13 +218,34 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
   }
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Gradient.  A block runs rows blockIdx.x, + gridDim.x, ... (WARP: a row per warp), so that each thread
 // keeps its columns' share of dgamma in registers; the block's sums go to one row of `part`, which
 // launch_colsum adds up in a fixed order (no atomics).
+//
+// A block's rows follow one another, so the next rows' loads have to be in flight while this one is
+// reduced: each thread copies its own 16-byte pieces of the next kGradStages - 1 rows to shared memory
+// asynchronously (it alone reads them, so no barrier is needed), which costs no registers.
+constexpr int grad_pieces(int vpt, bool h_f32) { return vpt * (1 + 2 * (h_f32 ? 2 : 1)); }
+constexpr int kGradStages = 3;
+// Rows beyond 16 elements a thread do not fit the ring: they are read twice, the second time from L2.
+constexpr bool grad_ring(int vpt, bool warp) { return vpt <= 2 || warp; }
+
 template <bool HF32, int VPT, bool WARP>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(const NormGradParams p) {
-  __shared__ float s_red[2][2][32];
-  extern __shared__ float s_part[];   // WARP: [warps - 1][d] shares of dgamma
+  __shared__ __align__(16) float2 s_red[2][kNormMaxThreads / 32];
+  extern __shared__ __align__(16) uint8_t s_dyn[];   // [stage][piece][thread] 16 bytes; then WARP: shares of dgamma
+  constexpr bool kRing = grad_ring(VPT, WARP);
+  constexpr int kP = grad_pieces(VPT, HF32);
+  constexpr int kH = HF32 ? 2 : 1;                   // pieces of one step of h or dh
   const int lane_t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int row_threads = WARP ? 32 : blockDim.x;
   const int warps = blockDim.x >> 5;
@@ -214,93 +253,142 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(const Nor
   const int64_t first = WARP ? static_cast<int64_t>(blockIdx.x) * warps + warp : blockIdx.x;
   const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * warps : gridDim.x;
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  float acc[VPT][kV];
+  const uint32_t ring = smem_u32(s_dyn) + threadIdx.x * 16;
+  const uint32_t piece_bytes = blockDim.x * 16;
+  constexpr int kSize = HF32 ? 4 : 2;
+  auto fetch = [&](int64_t n, int stage) {
+    if (!kRing) return;
+    if (n < p.N) {
+      const int64_t base = n * p.d;
+      const uint32_t dst = ring + stage * kP * piece_bytes;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * row_threads + lane_t) * kV;
+        if (c < p.d) {
+          const uint32_t at = dst + i * (1 + 2 * kH) * piece_bytes;
+          cp_async16(at, static_cast<const uint16_t*>(p.dy) + base + c);
+#pragma unroll
+          for (int k = 0; k < kH; ++k) {
+            cp_async16(at + (1 + k) * piece_bytes, static_cast<const uint8_t*>(p.h) + (base + c) * kSize + k * 16);
+            if (p.dh)
+              cp_async16(at + (1 + kH + k) * piece_bytes,
+                         static_cast<const uint8_t*>(p.dh) + (base + c) * kSize + k * 16);
+          }
+        }
+      }
+    }
+    cp_async_commit();   // one group per row, empty past the end
+  };
+  auto piece = [&](int stage, int i, int k) {
+    return s_dyn + static_cast<size_t>((stage * kP + i * (1 + 2 * kH) + k) * piece_bytes) + threadIdx.x * 16;
+  };
+  constexpr bool kKeep = VPT <= 2 || WARP;   // gamma and the row stay in registers
+  float acc[VPT][kV], gm[kKeep ? VPT : 1][kV];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * row_threads + lane_t) * kV;
 #pragma unroll
     for (int j = 0; j < kV; ++j) acc[i][j] = 0.f;
-  int flip = 0;
+    if (kKeep && c < p.d) load_gamma(p.gamma, p.gamma_f32, c, gm[i]);
+  }
+#pragma unroll
+  for (int k = 0; k < kGradStages - 1; ++k) fetch(first + k * step, k);
+  int flip = 0, stage = 0;
   for (int64_t n = first; n < p.N; n += step) {
     const int64_t base = n * p.d;
-    Pack<false> pdy[VPT];
-    Pack<HF32> ph[VPT], pdh[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * row_threads + lane_t) * kV;
-      if (c < p.d) {
-        pdy[i].load(p.dy, base + c);
-        ph[i].load(p.h, base + c);
-        if (p.dh) pdh[i].load(p.dh, base + c);
-      } else {
-        pdy[i].zero();
-        ph[i].zero();
-      }
-      if (c >= p.d || !p.dh) pdh[i].zero();
-    }
+    fetch(n + (kGradStages - 1) * step, stage == 0 ? kGradStages - 1 : stage - 1);
+    if (kRing) cp_async_wait<kGradStages - 1>();   // this row's pieces have landed
+    Pack<false> pdy[kKeep ? VPT : 1];
+    Pack<HF32> ph[kKeep ? VPT : 1];
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * row_threads + lane_t) * kV;
+      const int r = kKeep ? i : 0;
       if (c < p.d) {
-        float h[kV], dy[kV], g[kV];
-        ph[i].get(h);
-        pdy[i].get(dy);
-        load_gamma(p.gamma, p.gamma_f32, c, g);
+        if (kRing) {
+          pdy[r].load_pieces(piece(stage, i, 0), nullptr);
+          ph[r].load_pieces(piece(stage, i, 1), piece(stage, i, kH));
+        } else {
+          pdy[r].load(p.dy, base + c);
+          ph[r].load(p.h, base + c);
+          load_gamma(p.gamma, p.gamma_f32, c, gm[r]);
+        }
+        float h[kV], dy[kV];
+        ph[r].get(h);
+        pdy[r].get(dy);
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
           ss = fmaf(h[j], h[j], ss);
-          dot = fmaf(dy[j] * g[j], h[j], dot);
+          dot = fmaf(dy[j] * h[j], gm[r][j], dot);
         }
       }
     }
+    // both sums at once: lanes 0-15 go on with ss, lanes 16-31 with dot
+    {
+      const bool up = lane & 16;
+      const float mine = up ? dot : ss, other = up ? ss : dot;
+      float v = mine + __shfl_xor_sync(0xffffffffu, other, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      const float w = __shfl_xor_sync(0xffffffffu, v, 16);
+      ss = up ? w : v;
+      dot = up ? v : w;
     }
     if (!WARP) {
       // alternate buffers: a slot is rewritten two rows later, after the next row's barrier
-      if (lane == 0) {
-        s_red[flip][0][warp] = ss;
-        s_red[flip][1][warp] = dot;
-      }
+      if (lane == 0) s_red[flip][warp] = make_float2(ss, dot);
       __syncthreads();
-      ss = lane < warps ? s_red[flip][0][lane] : 0.f;
-      dot = lane < warps ? s_red[flip][1][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      ss = dot = 0.f;
+      for (int w = 0; w < warps; ++w) {
+        const float2 q = s_red[flip][w];
+        ss += q.x;
+        dot += q.y;
       }
       flip ^= 1;
     }
-    const float r = 1.0f / sqrtf(ss * inv_d + p.eps);
-    const float k = dot * inv_d * r * r;      // mean(a xhat) r = (dot / d) r^2 per unit of h
+    const float r = rsqrtf(ss * inv_d + p.eps);
+    const float rk = dot * inv_d * r * r * r;   // r mean(a xhat) per unit of xhat = (dot / d) r^3 per unit of h
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * row_threads + lane_t) * kV;
+      const int q = kKeep ? i : 0;
       if (c < p.d) {
-        float h[kV], dy[kV], g[kV], dh[kV], o[kV];
-        ph[i].get(h);
-        pdy[i].get(dy);
-        pdh[i].get(dh);
-        load_gamma(p.gamma, p.gamma_f32, c, g);
+        if (!kKeep) {
+          pdy[q].load(p.dy, base + c);
+          ph[q].load(p.h, base + c);
+          load_gamma(p.gamma, p.gamma_f32, c, gm[q]);
+        }
+        float h[kV], dy[kV], o[kV];
+        ph[q].get(h);
+        pdy[q].get(dy);
+        if (p.dh) {
+          Pack<HF32> pdh;
+          if (kRing) pdh.load_pieces(piece(stage, i, 1 + kH), piece(stage, i, 2 * kH));
+          else pdh.load(p.dh, base + c);
+          pdh.get(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kV; ++j) o[j] = 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
-          o[j] = fmaf(r, fmaf(-k, h[j], dy[j] * g[j]), dh[j]);
-          acc[i][j] = fmaf(dy[j], h[j] * r, acc[i][j]);
+          o[j] = fmaf(r * gm[q][j], dy[j], fmaf(-rk, h[j], o[j]));
+          acc[i][j] = fmaf(dy[j] * h[j], r, acc[i][j]);
         }
         Pack<HF32>::store(p.dx, base + c, o);
       }
     }
+    stage = stage + 1 == kGradStages ? 0 : stage + 1;
   }
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.d;
   if (WARP) {
+    float* shares = reinterpret_cast<float*>(s_dyn + static_cast<size_t>(kGradStages * kP) * piece_bytes);
     if (warp > 0) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (i * 32 + lane) * kV;
-        if (c < p.d) Pack<true>::store(s_part, static_cast<int64_t>(warp - 1) * p.d + c, acc[i]);
+        if (c < p.d) Pack<true>::store(shares, static_cast<int64_t>(warp - 1) * p.d + c, acc[i]);
       }
     }
     __syncthreads();
@@ -312,7 +400,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(const Nor
         if (c < p.d) {
           Pack<true> q;
           float o[kV];
-          q.load(s_part, static_cast<int64_t>(w) * p.d + c);
+          q.load(shares, static_cast<int64_t>(w) * p.d + c);
           q.get(o);
 #pragma unroll
           for (int j = 0; j < kV; ++j) acc[i][j] += o[j];
@@ -327,15 +415,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(const Nor
   }
 }
 
-// Column sums: 32 columns a block, 16 row groups, each summed in row order and then added up in order.
-constexpr int kColsumRows = 16;
+// Column sums: 32 columns a block, 32 row groups, each summed in row order and then added up in order.
+constexpr int kColsumRows = 32;
 __global__ void __launch_bounds__(32 * kColsumRows)
     colsum_kernel(const float* __restrict__ part, int rows, int n, float* __restrict__ out) {
   __shared__ float s[kColsumRows][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
   if (c < n) {
-#pragma unroll 8
+#pragma unroll 16
     for (int r = threadIdx.y; r < rows; r += kColsumRows) a += part[static_cast<int64_t>(r) * n + c];
   }
   s[threadIdx.y][threadIdx.x] = a;
@@ -355,24 +443,41 @@ struct NormShape {
   int threads;
 };
 
-// Steps per thread: a warp per row up to 1024 elements (no barrier); above, blocks of at most 256
-// threads when there are rows enough to fill the device (more rows in flight per SM), and the
-// fewest steps when there are few rows (the shortest chain of loads).
-NormShape norm_shape(int64_t N, int d, int sms) {
-  const int vecs = (d + kV - 1) / kV;
-  if (vecs <= 32 * 4 && N >= sms) {
-    int vpt = 1;
-    while (32 * vpt < vecs) vpt *= 2;
-    return {true, vpt, 32};
-  }
-  const int want = N > 2 * static_cast<int64_t>(sms) ? 256 : 512;
+NormShape block_shape(int vecs, int want) {
   int vpt = 1;
   while (vpt < 8 && (vecs + vpt - 1) / vpt > want) vpt *= 2;
-  const int threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
-  return {false, vpt, threads};
+  return {false, vpt, ((vecs + vpt - 1) / vpt + 31) / 32 * 32};
 }
 
-constexpr int kNormWarps = 4;   // rows of a block with a row per warp
+NormShape warp_shape(int vecs) {
+  int vpt = 1;
+  while (32 * vpt < vecs) vpt *= 2;
+  return {true, vpt, 32};
+}
+
+// Forward.  Up to 1024 elements and with rows enough, a warp per row: no barrier.  Above, with few rows the
+// fewest steps (the shortest chain of loads), else blocks of 256 threads, so that more rows are in flight per
+// SM; with an e4m3 output, whose second reduction makes each row's fixed cost twice as large, four steps from
+// 4096 elements on (142 against 165 us for 32768 x 4096).
+NormShape norm_shape(int64_t N, int d, bool e4m3, int sms) {
+  const int vecs = (d + kV - 1) / kV;
+  if (vecs <= 32 * 4 && N >= sms) return warp_shape(vecs);
+  if (N <= 2 * static_cast<int64_t>(sms) || vecs > 1024) return block_shape(vecs, kNormMaxThreads);
+  return block_shape(vecs, e4m3 && vecs >= 512 ? (vecs + 3) / 4 : 256);
+}
+
+// Gradient.  Two steps a thread wherever they hold the row (a warp per row up to 512 elements, with rows
+// enough): a row's fixed cost is shared by 16 elements, and the ring of the next rows fits beside it.
+NormShape norm_grad_shape(int64_t N, int d, int sms) {
+  const int vecs = (d + kV - 1) / kV;
+  if (vecs <= 64 && N >= 8 * static_cast<int64_t>(sms)) return warp_shape(vecs);
+  if (vecs > 1024) return block_shape(vecs, kNormMaxThreads);
+  return {false, 2, std::max(32, (vecs + 63) / 64 * 32)};
+}
+
+constexpr int kNormWarps = 4;       // rows of a block with a row per warp
+constexpr int kNormGradWarps = 4;
+constexpr int kGradSmemMax = 226 * 1024;
 
 template <bool XF32, bool HF32, bool Q>
 cudaError_t launch_norm(const NormParams& p, const NormShape& sh, cudaStream_t s) {
@@ -395,30 +500,62 @@ cudaError_t launch_norm(const NormParams& p, const NormShape& sh, cudaStream_t s
   return cudaGetLastError();
 }
 
+struct GradLaunch {
+  NormShape sh;
+  int threads, smem, sms;
+  int64_t rows;   // units of work: rows, or groups of rows with a row per warp
+  int grid;       // out: blocks launched
+};
+
+template <bool HF32, int VPT, bool WARP>
+cudaError_t grad_one(const NormGradParams& p, GradLaunch& g, cudaStream_t s) {
+  // warps that an SM's registers hold of this kernel; set with its shared-memory limit on the first launch
+  // on each device (past the 64th: on every launch)
+  static std::atomic<int> reg_warps[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int warps = dev < 64 ? reg_warps[dev].load(std::memory_order_acquire) : 0;
+  if (warps == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, rmsnorm_grad_kernel<HF32, VPT, WARP>);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(rmsnorm_grad_kernel<HF32, VPT, WARP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kGradSmemMax);
+    if (e != cudaSuccess) return e;
+    warps = 65536 / ((a.numRegs + 7) / 8 * 8 * 32);
+    if (dev < 64) reg_warps[dev].store(warps, std::memory_order_release);
+  }
+  // The grid is the blocks that are resident at once: each runs its share of the rows to the end, and one
+  // block more would run alone after all others.
+  const int per_sm = std::min({kGradSmemMax / (g.smem + 2048), warps / (g.threads / 32), 2048 / g.threads});
+  g.grid = static_cast<int>(
+      std::min<int64_t>({g.rows, kNormGradBlocks, static_cast<int64_t>(g.sms) * std::max(1, per_sm)}));
+  rmsnorm_grad_kernel<HF32, VPT, WARP><<<g.grid, g.threads, g.smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <bool HF32>
-cudaError_t launch_norm_grad(const NormGradParams& p, const NormShape& sh, int grid, cudaStream_t s) {
-  if (sh.warp) {
-    const size_t smem = static_cast<size_t>(kNormWarps - 1) * p.d * 4;
-    switch (sh.vpt) {
-      case 1: rmsnorm_grad_kernel<HF32, 1, true><<<grid, 32 * kNormWarps, smem, s>>>(p); break;
-      case 2: rmsnorm_grad_kernel<HF32, 2, true><<<grid, 32 * kNormWarps, smem, s>>>(p); break;
-      default: rmsnorm_grad_kernel<HF32, 4, true><<<grid, 32 * kNormWarps, smem, s>>>(p); break;
-    }
-  } else {
-    switch (sh.vpt) {
-      case 1: rmsnorm_grad_kernel<HF32, 1, false><<<grid, sh.threads, 0, s>>>(p); break;
-      case 2: rmsnorm_grad_kernel<HF32, 2, false><<<grid, sh.threads, 0, s>>>(p); break;
-      case 4: rmsnorm_grad_kernel<HF32, 4, false><<<grid, sh.threads, 0, s>>>(p); break;
-      default: rmsnorm_grad_kernel<HF32, 8, false><<<grid, sh.threads, 0, s>>>(p); break;
+cudaError_t launch_norm_grad(const NormGradParams& p, GradLaunch& g, cudaStream_t s) {
+  if (g.sh.warp) {
+    switch (g.sh.vpt) {
+      case 1: return grad_one<HF32, 1, true>(p, g, s);
+      case 2: return grad_one<HF32, 2, true>(p, g, s);
+      default: return grad_one<HF32, 4, true>(p, g, s);
     }
   }
-  return cudaGetLastError();
+  switch (g.sh.vpt) {
+    case 1: return grad_one<HF32, 1, false>(p, g, s);
+    case 2: return grad_one<HF32, 2, false>(p, g, s);
+    case 4: return grad_one<HF32, 4, false>(p, g, s);
+    default: return grad_one<HF32, 8, false>(p, g, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const NormParams& p, int sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.N, p.d, sms);
+  const NormShape sh = norm_shape(p.N, p.d, p.y_e4m3, sms);
   if (p.y_e4m3) {
     if (p.x_f32) return p.h_f32 ? launch_norm<true, true, true>(p, sh, s) : launch_norm<true, false, true>(p, sh, s);
     return p.h_f32 ? launch_norm<false, true, true>(p, sh, s) : launch_norm<false, false, true>(p, sh, s);
@@ -427,17 +564,17 @@ cudaError_t launch_rmsnorm(const NormParams& p, int sms, cudaStream_t s) {
   return p.h_f32 ? launch_norm<false, true, false>(p, sh, s) : launch_norm<false, false, false>(p, sh, s);
 }
 
-int rmsnorm_grad_blocks(int64_t N, int d, int sms) {
-  const NormShape sh = norm_shape(N, d, sms);
-  const int64_t rows = sh.warp ? (N + kNormWarps - 1) / kNormWarps : N;
-  const int64_t cap = std::min<int64_t>(kNormGradBlocks, static_cast<int64_t>(sms) * 4);
-  return static_cast<int>(std::min(rows, cap));
-}
-
-cudaError_t launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s) {
-  const NormShape sh = norm_shape(p.N, p.d, sms);
-  const int grid = rmsnorm_grad_blocks(p.N, p.d, sms);
-  return p.h_f32 ? launch_norm_grad<true>(p, sh, grid, s) : launch_norm_grad<false>(p, sh, grid, s);
+int launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s, cudaError_t* err) {
+  GradLaunch g;
+  g.sh = norm_grad_shape(p.N, p.d, sms);
+  g.threads = g.sh.warp ? 32 * kNormGradWarps : g.sh.threads;
+  g.smem = (grad_ring(g.sh.vpt, g.sh.warp) ? kGradStages * grad_pieces(g.sh.vpt, p.h_f32) * g.threads * 16 : 0) +
+           (g.sh.warp ? (kNormGradWarps - 1) * p.d * 4 : 0);
+  g.rows = g.sh.warp ? (p.N + kNormGradWarps - 1) / kNormGradWarps : p.N;
+  g.sms = sms;
+  g.grid = 0;
+  *err = p.h_f32 ? launch_norm_grad<true>(p, g, s) : launch_norm_grad<false>(p, g, s);
+  return g.grid;
 }
 
 cudaError_t launch_colsum(const float* part, int rows, int n, float* out, cudaStream_t s) {

@@ -120,6 +120,29 @@ def test_many_tiles_per_pair():
     assert torch.equal(p0, p1) and torch.equal(y0, y1)   # each output is one fp32 reduction in the same order
 
 
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("plan", [20128, 30192, 40256, 50128, 70256, 80192])
+def test_split_last_wave(plan, f8):
+    """Tiles whose reduction is shared by several CTA pairs and joined through the workspace."""
+    o = _data(300, 4112 if f8 else 2088, 712, f8, seed=10)     # 33 reduction blocks, the last partly filled
+    _check(o, "silu", pre=True, plan=plan)
+    _check(o, "none", bias=False, residual=False, plan=plan)
+    a, pa = _call(o, "gelu", pre=True, plan=plan)
+    for _ in range(3):                                         # whichever share arrives last, the same bits
+        b, pb = _call(o, "gelu", pre=True, plan=plan)
+        assert torch.equal(a, b) and torch.equal(pa, pb)
+
+
+def test_split_last_wave_after_full_waves():
+    """180 tiles: two full waves of 74 pairs and 32 tiles in two shares each."""
+    o = _data(5000, 576, 2088, seed=11)
+    _check(o, "gelu_tanh", pre=True, plan=20256, rows=slice(0, 300))
+    _check(o, "gelu_tanh", pre=True, plan=20256, rows=slice(4700, 5000))
+    a, _ = _call(o, "silu", plan=20256)
+    b, _ = _call(o, "silu", plan=256)
+    assert (a.float() - b.float()).abs().max().item() <= 2.0 ** -6 * b.float().abs().max().item()
+
+
 def test_splits_leave_rounding_only():
     """Splitting the reduction changes the order of one fp32 sum: results stay within its bound, and repeat."""
     o = _data(40, 2048, 512, seed=5)
@@ -160,11 +183,12 @@ def test_nonfinite_rows_stay_in_their_rows(M):
 @pytest.mark.parametrize("M", [5, 300])
 def test_residual_in_place(M):
     o = _data(M, 256, 264, seed=8)
-    want, _ = _call(o, "gelu")
-    y = o["residual"].clone()
-    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
-    K.kdkl_linear_forward(o["x"], o["W"], y, ws, bias=o["bias"], residual=y, activation="gelu")
-    assert torch.equal(y, want)
+    ws = torch.empty(K.kdkl_linear_workspace_bytes(M, 256, 264), dtype=torch.uint8, device="cuda")
+    for plan in (0, 256, 4032):
+        y = o["residual"].clone()
+        want, _ = _call(o, "gelu", plan=plan)
+        K.kdkl_linear_forward(o["x"], o["W"], y, ws, bias=o["bias"], residual=y, activation="gelu", plan=plan)
+        assert torch.equal(y, want)
 
 
 def test_offsets_past_32_bits():
@@ -177,7 +201,7 @@ def test_offsets_past_32_bits():
     W = (torch.randn(d_out, d_in, generator=g, device="cuda") / 4).to(BF)
     y = torch.empty(M, d_out, dtype=BF, device="cuda")
     y[-300:].fill_(9)
-    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(K.kdkl_linear_workspace_bytes(M, d_in, d_out), dtype=torch.uint8, device="cuda")
     K.kdkl_linear_forward(x, W, y, ws, residual=y, activation="none")     # residual read at the same offsets
     want = _f64(x[-300:]) @ _f64(W).T + 9
     S = np.abs(_f64(x[-300:])) @ np.abs(_f64(W)).T + 9
@@ -245,6 +269,17 @@ def test_every_dx_plan(dx_plan):
     _check_grad(*_grad_data(1, 8, 520, seed=3), "none", dx_plan=dx_plan, want=("dx",))
 
 
+def test_split_gradient_products():
+    dy, pre, x, W = _grad_data(2100, 712, 1096, seed=9)
+    for dx_plan, dw_plan in ((20256, 20256), (40192, 30192), (20128, 20128)):
+        _check_grad(dy[:300], pre[:300], x[:300], W, "silu", dx_plan=dx_plan, want=("dx",))
+        _check_grad(dy, pre, x, W, "silu", dw_plan=dw_plan, want=("dW",))
+    both = _grad(dy, pre, x, W, "gelu", dx_plan=20256, dw_plan=40256)
+    for _ in range(2):
+        again = _grad(dy, pre, x, W, "gelu", dx_plan=20256, dw_plan=40256)
+        assert all(torch.equal(a, b) for a, b in zip(both, again))
+
+
 @pytest.mark.parametrize("dw_plan", PAIR_PLANS)
 def test_every_dw_plan(dw_plan):
     _check_grad(*_grad_data(300, 712, 536, seed=4), "silu", dw_plan=dw_plan, want=("dW",))
@@ -293,7 +328,7 @@ def test_empty_batch():
 def test_binding_refusals():
     o = _data(10, 64, 128)
     y = torch.empty(10, 128, dtype=BF, device="cuda")
-    ws = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(K.kdkl_linear_workspace_bytes(10, 64, 128) + 256, dtype=torch.uint8, device="cuda")
 
     def refused(match, **kw):
         a = dict(x=o["x"], W=o["W"], y=y, ws=ws)
@@ -311,13 +346,16 @@ def test_binding_refusals():
     refused("is no plan", plan=2016)          # d_in = 64 has one reduction block, not two
     refused("is no plan", plan=3016)
     refused("is no plan", plan=1048)
+    refused("is no plan", plan=20256)         # one reduction block cannot be split
+    refused("is no plan", plan=-256)
+    refused("is no plan", plan=90256)
     refused("need x_scale", x=o["x"].to(F8), W=o["W"].to(F8))
     refused("KDKL_E4M3 operands only", x_scale=torch.ones(10, device="cuda"))
     refused("workspace is on cpu", ws=ws.cpu())
     refused("KDKL_ERR_WORKSPACE", ws=ws[:128])
     refused("KDKL_ERR_ALIGN", ws=ws[8:])
     dW = torch.empty(128, 64, dtype=BF, device="cuda")
-    big = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    big = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
     with pytest.raises(K.KDKLError, match="is no plan"):
         K.kdkl_linear_backward(y, o["x"], o["W"], None, dW, big, dw_plan=1016)
     with pytest.raises(K.KDKLError, match="needs pre"):

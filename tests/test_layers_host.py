@@ -80,7 +80,7 @@ def test_linear_forward_refusals(lib):
     assert _fwd(lib, d_out=(1 << 20) + 8) == UNSUPPORTED
     for name in ("x", "W", "bias", "residual", "y", "pre"):
         assert _fwd(lib, **{name: 0x80008}) == ALIGN
-    assert _fwd(lib, ws=0x80010) == ALIGN and _fwd(lib, wsb=255) == WORKSPACE
+    assert _fwd(lib, ws=0x80010) == ALIGN and _fwd(lib, wsb=K.kdkl_linear_workspace_bytes(100, 256, 128) - 1) == WORKSPACE
     assert _fwd(lib, opt=dict(activation=5)) == UNSUPPORTED and _fwd(lib, opt=dict(activation=-1)) == UNSUPPORTED
     assert _fwd(lib, opt=dict(operands=K.F32)) == UNSUPPORTED
     f8 = dict(operands=K.E4M3, x_scale=0x90000, w_scale=0xA0000)
@@ -117,6 +117,8 @@ def test_linear_backward_refusals(lib):
 def test_linear_plans(lib):
     def plan(*a, **kw):
         return K.kdkl_linear_plan(*a, sm_count=148, **kw)
+    # half the last wave's pairs idle: its tiles are split
+    assert plan(1 << 14, 4096, 4096, product=K.LINEAR_DW) == 20256
     # few rows: small tiles, the reduction split; many rows: full 256 x 256 tiles
     assert plan(1, 4096, 4096) > 1000 and plan(1, 4096, 4096) % 1000 == 16
     assert plan(32768, 4096, 4096) == 256
@@ -125,8 +127,12 @@ def test_linear_plans(lib):
         for d_in, d_out in ((16, 8), (64, 4096), (4096, 64), (2048, 2880), (4096, 4096), (1 << 20, 1 << 20)):
             for ops, prod in ((K.BF16, 0), (K.E4M3, 0), (K.BF16, 1), (K.BF16, 2)):
                 p = plan(M, d_in, d_out, operands=ops, product=prod)
-                if p < 1000:
-                    assert p in (128, 192, 256)
+                if p % 10000 in (128, 192, 256):
+                    # the last wave's tiles split 2 to 8 ways, each share of 4 reduction blocks at least
+                    rows, cols, length = ((M, d_out, d_in), (M, d_in, d_out), (d_out, d_in, M))[prod]
+                    tail = -(-rows // 256) * -(-cols // (p % 10000)) % 74
+                    blocks = -(-length // (128 if ops == K.E4M3 else 64))
+                    assert p < 10000 or 2 <= p // 10000 <= min(8, 74 // tail, blocks // 4)
                 else:
                     length = d_out if prod == 1 else d_in
                     assert prod != 2 and p % 1000 in (16, 32, 64, 128) and p // 1000 in (1, 2, 4, 8)
