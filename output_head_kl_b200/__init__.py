@@ -174,9 +174,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_torch = None
+
+
+def _import_torch():
+    """torch, imported on first use (the library itself does not need it)."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
+        torch = _torch or _import_torch()
         # the handle of torch.cuda.current_stream(), without building a Stream object for it
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -393,7 +404,7 @@ def _tensor(where, name, t, shape, dtypes, dev) -> int | None:
 
 def _where(where, t, name):
     """torch and the current device's index, after checking that `t`, of two dimensions, is on that device."""
-    import torch
+    torch = _torch or _import_torch()
     if t.dim() != 2:
         _bad(2, where, f"{name} has {t.dim()} dimensions, expected 2")
     dev = t.get_device()
