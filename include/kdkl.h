@@ -421,9 +421,10 @@ typedef struct {
   const float* x_scale;  /* KDKL_E4M3: [M] fp32 */
   const float* w_scale;  /* KDKL_E4M3: [d_out] fp32 */
   /* Tiles of the products: 0 = the planner's choice (default), else a plan as kdkl_linear_plan reports it.
-   * 128, 192 or 256: tiles of 256 rows x that many columns, by CTA pairs; + 10000 * splits (2 to 8): the tiles
-   * of the last, partly filled wave of pairs are each split into that many shares of the reduction, as far as
-   * all shares run at once and keep 4 reduction blocks (128 bytes of a row; of dW, 64 rows) each.
+   * 128, 192 or 256: tiles of 256 rows x that many columns, by CTA pairs; + 10000 * splits: the tiles of the
+   * last, partly filled wave of pairs are each split into that many shares of the reduction (2 to 8; 2 or 4
+   * where the product has no full wave, dW excepted), as far as all shares run at once and keep 4 reduction
+   * blocks (128 bytes of a row; of dW, 64 rows) each.
    * 1000 * splits + rows (splits 1, 2, 4 or 8, at most one per reduction block; rows 16, 32, 64 or 128): tiles
    * of 128 columns x `rows` rows, the reduction split over a cluster of `splits` CTAs; not for dW. */
   int32_t plan;          /* forward */

@@ -51,14 +51,18 @@ struct Plan {
 // Tiles of the last, partly filled wave of large tiles (0 when every wave is full).
 int64_t tail_tiles(int64_t tiles, int sms) { return tiles % (sms / 2); }
 
-// The most shares that each tile of the last wave can be split into: all shares run at once, and each
-// keeps at least four reduction blocks.
-int most_splits(int64_t tail, int k_blocks, int sms) {
-  if (tail == 0) return 1;
-  const int64_t units = std::min<int64_t>(sms / 2, kMaxShares);
-  const int64_t s = std::min<int64_t>({units / tail, k_blocks / 4, kMaxTailSplits});
-  return static_cast<int>(std::max<int64_t>(s, 1));
+// Whether the tiles of the last wave can each be split into `sp` shares of the reduction: all shares run at
+// once and keep at least four reduction blocks.  Where there is no full wave, a cluster of 2 or 4 pairs shares
+// each tile (dW: any number of shares, by way of the workspace, as after full waves).
+bool can_split(LinOp op, int64_t tiles, int k_blocks, int sms, int sp) {
+  const int64_t tail = tail_tiles(tiles, sms);
+  if (sp < 2 || sp > kMaxTailSplits || tail == 0 || k_blocks / sp < 4) return false;
+  if (tail * sp > std::min<int64_t>(sms / 2, kMaxShares)) return false;
+  return op == kLinDw || tail < tiles || sp == 2 || sp == 4;
 }
+
+// Splits by clusters, without the workspace.
+bool cluster_split(LinOp op, int64_t tiles, int sms, int sp) { return sp > 1 && op != kLinDw && tiles < sms / 2; }
 
 // Product out[rows, cols] with `k_blocks` reduction blocks.
 //
@@ -79,11 +83,11 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
     const double epilogue = 1.57 * bn / 256;
     const int64_t tiles = rb * ((cols + bn - 1) / bn);
     const int64_t tail = tail_tiles(tiles, sms), full = tiles / pairs;
-    const int most = most_splits(tail, k_blocks, sms);
-    for (int sp = 1; sp <= most; ++sp) {
+    for (int sp = 1; sp <= kMaxTailSplits; ++sp) {
+      if (sp > 1 && !can_split(op, tiles, k_blocks, sms, sp)) continue;
       double t = 2.04 + 4.43 * bn / 256 + static_cast<double>(full) * (k_blocks * kb + epilogue);
       if (tail) t += (k_blocks + sp - 1) / sp * kb + (full ? epilogue : 0.0);
-      if (sp > 1) t += 13.2 + 0.76 * sp;
+      if (sp > 1) t += cluster_split(op, tiles, sms, sp) ? 1.0 : 13.2 + 0.76 * sp;
       if (t < lo) {
         lo = t;
         best = Plan{true, bn, sp};
@@ -117,7 +121,7 @@ bool decode_plan(int32_t code, LinOp op, int64_t rows, int64_t cols, int k_block
     const int sp = code / 10000;
     p = Plan{true, bn, sp == 0 ? 1 : sp};
     const int64_t tiles = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
-    return sp == 0 || (sp >= 2 && sp <= most_splits(tail_tiles(tiles, sms), k_blocks, sms));
+    return sp == 0 || can_split(op, tiles, k_blocks, sms, sp);
   }
   if (op == kLinDw || code < 1000) return false;
   const int sp = code / 1000, nt = code % 1000;
@@ -153,7 +157,7 @@ kdkl_linear_options default_linear_options() {
 }
 
 struct LinearLayout {
-  size_t tickets = 0, shares = 0, dz = 0, part = 0, total = 0;
+  size_t tickets = 0, col_tickets = 0, shares = 0, dz = 0, part = 0, total = 0;
 };
 
 // Bytes of the partial sums that a product out[rows, cols] may split its last wave into, whatever its tile
@@ -163,12 +167,14 @@ size_t share_bytes(int64_t rows, int64_t cols) {
   return static_cast<size_t>(std::min<int64_t>(kMaxShares, tiles * kMaxTailSplits)) * kShareBytes;
 }
 
-// Workspace: the flag word, the tickets and partial sums of split tiles; for the gradient also dz and the
-// partial column sums of the most blocks act_grad runs.
+// Workspace: the flag word and the tickets (everything before `shares` is cleared ahead of the launches that
+// use it), the partial sums of split tiles; for the gradient also dz and the partial column sums of the most
+// blocks act_grad runs.
 LinearLayout linear_layout(int64_t M, int32_t d_in, int32_t d_out, bool backward) {
   LinearLayout L;
   L.tickets = kFlagBytes;
-  L.shares = align_up(L.tickets + kTicketBytes, 256);
+  L.col_tickets = L.tickets + kTicketBytes;
+  L.shares = align_up(L.col_tickets + (backward ? static_cast<size_t>((d_out + 255) / 256) * 4 : 0), 256);
   size_t off = L.shares + (backward ? std::max(share_bytes(M, d_in), share_bytes(d_out, d_in))
                                     : share_bytes(M, d_out));
   if (backward) {
@@ -216,6 +222,7 @@ cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b
     if ((p.pre && !box(&m.pre, p.pre)) || (p.residual && !box(&m.res, p.residual))) return cudaErrorInvalidValue;
     p.n_tiles = static_cast<int>((cols + bn - 1) / bn);
     p.tiles = static_cast<int>((rows + 255) / 256) * p.n_tiles;
+    if (cluster_split(op, p.tiles, sms, plan.splits)) return launch_linear_split(op, bn, m, p, s);
     const int tail = plan.splits > 1 ? static_cast<int>(tail_tiles(p.tiles, sms)) : 0;
     p.full_units = p.tiles - tail;
     p.units = p.full_units + tail * plan.splits;
@@ -266,8 +273,8 @@ kdkl_status device_with_pairs(Device& dv) {
 }
 
 // Clears the flag word and the tickets of split tiles ahead of the launches.
-kdkl_status clear_header(void* workspace, cudaStream_t s) {
-  const cudaError_t e = cudaMemsetAsync(workspace, 0, kFlagBytes + kTicketBytes, s);
+kdkl_status clear_header(void* workspace, const LinearLayout& L, cudaStream_t s) {
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, L.shares, s);
   return e == cudaSuccess ? KDKL_OK : cuda_fail(e, "cudaMemsetAsync");
 }
 
@@ -428,8 +435,10 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   Plan plan;
   if ((st = pick_plan(o.plan, op, M, d_out, d_in, dv.sms, "plan", plan)) != KDKL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool clear_ahead = kClearAhead || M == 0 || (plan.pair && plan.splits > 1);
-  if (clear_ahead && (st = clear_header(workspace, s)) != KDKL_OK) return st;
+  const int64_t tiles = plan.pair ? ((M + 255) / 256) * ((d_out + plan.tile - 1) / plan.tile) : 0;
+  const bool clear_ahead =
+      kClearAhead || M == 0 || (plan.pair && plan.splits > 1 && !cluster_split(op, tiles, dv.sms, plan.splits));
+  if (clear_ahead && (st = clear_header(workspace, L, s)) != KDKL_OK) return st;
   if (M == 0) return ok();
   LinParams p = {};
   p.bias = static_cast<const uint16_t*>(bias);
@@ -477,7 +486,7 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   if (dW && (st = pick_plan(o.dw_plan, kLinDw, d_out, d_in, M, dv.sms, "dw_plan", dw_plan)) != KDKL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if ((st = clear_header(workspace, s)) != KDKL_OK) return st;
+  if ((st = clear_header(workspace, L, s)) != KDKL_OK) return st;
   if (M == 0) {
     if (dW && (e = cudaMemsetAsync(dW, 0, static_cast<size_t>(d_out) * d_in * 2, s)) != cudaSuccess)
       return cuda_fail(e, "cudaMemsetAsync");
@@ -489,12 +498,11 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   const void* dz = dy;
   if (act || dbias) {
     uint16_t* dz_out = act && (dx || dW) ? reinterpret_cast<uint16_t*>(ws + L.dz) : nullptr;
-    float* part = dbias ? reinterpret_cast<float*>(ws + L.part) : nullptr;
-    const int chunks = act_grad_chunks(M, d_out, dv.sms);
     e = timed(kTActGrad, s, [&] {
-      const cudaError_t e1 = launch_act_grad(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre),
-                                             o.activation, M, d_out, dz_out, part, chunks, s);
-      return e1 != cudaSuccess || !dbias ? e1 : launch_colsum(part, chunks, d_out, dbias, s);
+      return launch_act_grad(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre), o.activation, M,
+                             d_out, dz_out, reinterpret_cast<float*>(ws + L.part),
+                             reinterpret_cast<uint32_t*>(ws + L.col_tickets), dbias,
+                             act_grad_chunks(M, d_out, dv.sms), s);
     });
     if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");
     if (act) dz = ws + L.dz;

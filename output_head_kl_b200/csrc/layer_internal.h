@@ -86,16 +86,40 @@ struct PairMaps {
   CUtensorMap out, pre, res;  // 32 x 32 boxes of y, z and the residual (unused ones repeat `out`)
 };
 cudaError_t launch_linear_pair(int op, int bn, const PairMaps& m, const LinParams& p, int grid, cudaStream_t s);
+// The same tiles, each shared by a cluster of p.splits (2 or 4) pairs that split its reduction; all but kLinDw.
+cudaError_t launch_linear_split(int op, int bn, const PairMaps& m, const LinParams& p, cudaStream_t s);
 // Small tiles: 128 output columns x nt rows (nt = 16, 32, 64 or 128) per cluster of p.splits CTAs; the
 // roles of the operands are swapped (tmA reads W, tmB reads x or dz).  op: all but kLinDw.
 cudaError_t launch_linear_small(int op, int nt, const CUtensorMap& tmA, const CUtensorMap& tmB, const LinParams& p,
                                 cudaStream_t s);
 
-// dz = dy * act'(pre) in bf16 (dz may be null: column sums only, of dy when act is none) and the
-// partial column sums part[chunks, n] of its fp32 values (part may be null).
-constexpr int kMaxSms = 512;   // workspaces are sized for any device up to this many SMs
+// dz = dy * act'(pre) in bf16 (dz may be null: column sums only, of dy when act is none) and, with dbias, the
+// column sums of its fp32 values, by way of part[chunks, n] and one ticket per 256 columns (zero before).
+constexpr int kMaxSms = 512;         // workspaces are sized for any device up to this many SMs
+constexpr int kMaxActChunks = 256;   // row ranges that the last block of a column range adds up
 int act_grad_chunks(int64_t M, int n, int sms);
 cudaError_t launch_act_grad(const uint16_t* dy, const uint16_t* pre, int act, int64_t M, int n, uint16_t* dz,
-                            float* part, int chunks, cudaStream_t s);
+                            float* part, uint32_t* tickets, float* dbias, int chunks, cudaStream_t s);
+
+// Launch configuration of these kernels: all of them wait for the kernels before them by themselves
+// (pdl_wait), so that their set-up overlaps the end of the one before.
+struct LaunchConfig {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t c;
+  LaunchConfig(dim3 grid, dim3 block, int smem, int cluster, cudaStream_t s) : attr{}, c{} {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = static_cast<size_t>(smem);
+    c.stream = s;
+    c.attrs = attr;
+    c.numAttrs = cluster > 0 ? 2 : 1;
+  }
+  LaunchConfig(const LaunchConfig&) = delete;
+};
 
 }  // namespace kdkl

@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
   const int row_threads = WARP ? 32 : blockDim.x;
   const int warps = blockDim.x >> 5;
   const int64_t n = WARP ? static_cast<int64_t>(blockIdx.x) * warps + (threadIdx.x >> 5) : blockIdx.x;
+  pdl_wait();
+  pdl_launch();
   if (WARP && n >= p.N) return;
   const int64_t base = n * p.d;
   float v[VPT][kV];
@@ -282,6 +284,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_grad_kernel(const Nor
   auto piece = [&](int stage, int i, int k) {
     return s_dyn + static_cast<size_t>((stage * kP + i * (1 + 2 * kH) + k) * piece_bytes) + threadIdx.x * 16;
   };
+  pdl_wait();
+  pdl_launch();
   constexpr bool kKeep = VPT <= 2 || WARP;   // gamma and the row stay in registers
   float acc[VPT][kV], gm[kKeep ? VPT : 1][kV];
 #pragma unroll
@@ -420,6 +424,8 @@ constexpr int kColsumRows = 32;
 __global__ void __launch_bounds__(32 * kColsumRows)
     colsum_kernel(const float* __restrict__ part, int rows, int n, float* __restrict__ out) {
   __shared__ float s[kColsumRows][33];
+  pdl_wait();
+  pdl_launch();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float a = 0.f;
   if (c < n) {
@@ -482,22 +488,21 @@ constexpr int kGradSmemMax = 226 * 1024;
 template <bool XF32, bool HF32, bool Q>
 cudaError_t launch_norm(const NormParams& p, const NormShape& sh, cudaStream_t s) {
   if (sh.warp) {
-    const unsigned grid = static_cast<unsigned>((p.N + kNormWarps - 1) / kNormWarps);
+    const LaunchConfig cfg(dim3(static_cast<unsigned>((p.N + kNormWarps - 1) / kNormWarps)), dim3(32 * kNormWarps), 0,
+                           0, s);
     switch (sh.vpt) {
-      case 1: rmsnorm_kernel<XF32, HF32, Q, 1, true><<<grid, 32 * kNormWarps, 0, s>>>(p); break;
-      case 2: rmsnorm_kernel<XF32, HF32, Q, 2, true><<<grid, 32 * kNormWarps, 0, s>>>(p); break;
-      default: rmsnorm_kernel<XF32, HF32, Q, 4, true><<<grid, 32 * kNormWarps, 0, s>>>(p); break;
-    }
-  } else {
-    const unsigned grid = static_cast<unsigned>(p.N);
-    switch (sh.vpt) {
-      case 1: rmsnorm_kernel<XF32, HF32, Q, 1, false><<<grid, sh.threads, 0, s>>>(p); break;
-      case 2: rmsnorm_kernel<XF32, HF32, Q, 2, false><<<grid, sh.threads, 0, s>>>(p); break;
-      case 4: rmsnorm_kernel<XF32, HF32, Q, 4, false><<<grid, sh.threads, 0, s>>>(p); break;
-      default: rmsnorm_kernel<XF32, HF32, Q, 8, false><<<grid, sh.threads, 0, s>>>(p); break;
+      case 1: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 1, true>, p);
+      case 2: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 2, true>, p);
+      default: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 4, true>, p);
     }
   }
-  return cudaGetLastError();
+  const LaunchConfig cfg(dim3(static_cast<unsigned>(p.N)), dim3(sh.threads), 0, 0, s);
+  switch (sh.vpt) {
+    case 1: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 1, false>, p);
+    case 2: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 2, false>, p);
+    case 4: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 4, false>, p);
+    default: return cudaLaunchKernelEx(&cfg.c, rmsnorm_kernel<XF32, HF32, Q, 8, false>, p);
+  }
 }
 
 struct GradLaunch {
@@ -531,8 +536,8 @@ cudaError_t grad_one(const NormGradParams& p, GradLaunch& g, cudaStream_t s) {
   const int per_sm = std::min({kGradSmemMax / (g.smem + 2048), warps / (g.threads / 32), 2048 / g.threads});
   g.grid = static_cast<int>(
       std::min<int64_t>({g.rows, kNormGradBlocks, static_cast<int64_t>(g.sms) * std::max(1, per_sm)}));
-  rmsnorm_grad_kernel<HF32, VPT, WARP><<<g.grid, g.threads, g.smem, s>>>(p);
-  return cudaGetLastError();
+  const LaunchConfig cfg(dim3(g.grid), dim3(g.threads), g.smem, 0, s);
+  return cudaLaunchKernelEx(&cfg.c, rmsnorm_grad_kernel<HF32, VPT, WARP>, p);
 }
 
 template <bool HF32>
@@ -578,8 +583,8 @@ int launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s, cudaEr
 }
 
 cudaError_t launch_colsum(const float* part, int rows, int n, float* out, cudaStream_t s) {
-  colsum_kernel<<<(n + 31) / 32, dim3(32, kColsumRows), 0, s>>>(part, rows, n, out);
-  return cudaGetLastError();
+  const LaunchConfig cfg(dim3((n + 31) / 32), dim3(32, kColsumRows), 0, 0, s);
+  return cudaLaunchKernelEx(&cfg.c, colsum_kernel, part, rows, n, out);
 }
 
 }  // namespace kdkl

@@ -351,6 +351,14 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask) {
       : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// With the stream-serialisation attribute a kernel may start while the one before it on the stream ends:
+// pdl_wait returns once every earlier kernel has finished and its writes are visible (at once in an ordinary
+// launch), so it stands before the first access to global memory of every thread; pdl_launch lets
+// the next kernel start its own set-up.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- math
 // 2^x on the special-function unit (the PTX instruction, no library code).
 __device__ __forceinline__ float ex2_approx(float x) {

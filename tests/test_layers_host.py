@@ -132,7 +132,10 @@ def test_linear_plans(lib):
                     rows, cols, length = ((M, d_out, d_in), (M, d_in, d_out), (d_out, d_in, M))[prod]
                     tail = -(-rows // 256) * -(-cols // (p % 10000)) % 74
                     blocks = -(-length // (128 if ops == K.E4M3 else 64))
-                    assert p < 10000 or 2 <= p // 10000 <= min(8, 74 // tail, blocks // 4)
+                    sp = p // 10000
+                    full = -(-rows // 256) * -(-cols // (p % 10000)) >= 74
+                    assert sp == 0 or 2 <= sp <= min(8, 74 // tail, blocks // 4)
+                    assert sp in (0, 2, 4) or full or prod == 2
                 else:
                     length = d_out if prod == 1 else d_in
                     assert prod != 2 and p % 1000 in (16, 32, 64, 128) and p // 1000 in (1, 2, 4, 8)
