@@ -51,6 +51,10 @@ struct Plan {
 // Tiles of the last, partly filled wave of large tiles (0 when every wave is full).
 int64_t tail_tiles(int64_t tiles, int sms) { return tiles % (sms / 2); }
 
+// Clusters of 4 or 8 CTAs with an SM each that run at once: a cluster stays within one GPC, so some SMs are
+// left over (B200, 148 SMs: 33 and 15 were found resident; one less is counted on).
+int64_t cluster_slots(int sms, int ctas) { return static_cast<int64_t>(ctas == 4 ? 32 : 14) * sms / 148; }
+
 // Whether the tiles of the last wave can each be split into `sp` shares of the reduction: all shares run at
 // once and keep at least four reduction blocks.  Where there is no full wave, a cluster of 2 or 4 pairs shares
 // each tile (dW: any number of shares, by way of the workspace, as after full waves).
@@ -58,7 +62,8 @@ bool can_split(LinOp op, int64_t tiles, int k_blocks, int sms, int sp) {
   const int64_t tail = tail_tiles(tiles, sms);
   if (sp < 2 || sp > kMaxTailSplits || tail == 0 || k_blocks / sp < 4) return false;
   if (tail * sp > std::min<int64_t>(sms / 2, kMaxShares)) return false;
-  return op == kLinDw || tail < tiles || sp == 2 || sp == 4;
+  if (op == kLinDw || tail < tiles) return true;
+  return (sp == 2 || sp == 4) && tiles <= cluster_slots(sms, 2 * sp);
 }
 
 // Splits by clusters, without the workspace.
@@ -67,11 +72,12 @@ bool cluster_split(LinOp op, int64_t tiles, int sms, int sp) { return sp > 1 && 
 // Product out[rows, cols] with `k_blocks` reduction blocks.
 //
 // Cost model in microseconds; its constants are a fit to the measured times of every plan of the forward at
-// 196 sizes (rows 1 to 4096, widths 256 to 8192, bf16 and e4m3): the plan it picks is on average 1 % and at
-// most 15 % slower than the fastest one there.
+// 196 sizes (rows 1 to 4096, widths 256 to 8192, bf16 and e4m3): there the plan it picks is 1.5 % slower than
+// the fastest one on average and 22 % at worst.
 //   pair tiles:  launch + last epilogue + per tile of a pair: kb[bn] per reduction block (a 256-wide
 //                tile's two operands fill what an SM can take in from L2, so narrower ones cost nearly as
-//                much) and the epilogue's share; splitting the last wave's tiles costs their join.
+//                much) and the epilogue's share.  Splitting the last wave's tiles costs their join by way of the
+//                workspace; a cluster's join shares out the epilogue and saves some of it.
 //   small tiles: launch, join and, per wave of two CTAs an SM, kb + kb_row per row of the tile.
 Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
   Plan best;
@@ -79,15 +85,15 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
   const int pairs = sms / 2;
   const int64_t rb = (rows + 255) / 256;
   for (int bn : {256, 192, 128}) {
-    const double kb = bn == 256 ? 0.247 : (bn == 192 ? 0.233 : 0.219);
-    const double epilogue = 1.57 * bn / 256;
+    const double kb = bn == 256 ? 0.321 : (bn == 192 ? 0.277 : 0.237);
+    const double width = bn / 256.0;
     const int64_t tiles = rb * ((cols + bn - 1) / bn);
     const int64_t tail = tail_tiles(tiles, sms), full = tiles / pairs;
     for (int sp = 1; sp <= kMaxTailSplits; ++sp) {
       if (sp > 1 && !can_split(op, tiles, k_blocks, sms, sp)) continue;
-      double t = 2.04 + 4.43 * bn / 256 + static_cast<double>(full) * (k_blocks * kb + epilogue);
-      if (tail) t += (k_blocks + sp - 1) / sp * kb + (full ? epilogue : 0.0);
-      if (sp > 1) t += cluster_split(op, tiles, sms, sp) ? 1.0 : 13.2 + 0.76 * sp;
+      double t = 3.26 + 5.72 * width + static_cast<double>(full) * (k_blocks * kb + 0.441 * width);
+      if (tail) t += (k_blocks + sp - 1) / sp * kb + (full ? 0.441 * width : 0.0);
+      if (sp > 1) t += cluster_split(op, tiles, sms, sp) ? 1.85 - 3.13 * width : 9.74 + 0.488 * sp;
       if (t < lo) {
         lo = t;
         best = Plan{true, bn, sp};
@@ -100,11 +106,13 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
     for (int sp : {1, 2, 4, 8}) {
       const int64_t ctas = tiles * sp;
       if (sp > k_blocks || ctas > INT_MAX / 2) break;
-      const int64_t waves = (ctas + 2 * sms - 1) / (2 * sms);
-      const double share = ctas <= sms ? 1.0 : (waves == 1 ? 1.8 : 2.0);   // two CTAs share an SM's intake
-      const double block = (0.227 + 0.0904 * nt / 64) * share;
-      const double t = 3.22 + 0.114 * sp + 0.486 * nt / (64.0 * sp) +
-                       static_cast<double>(waves) * ((k_blocks + sp - 1) / sp * block + 0.627);
+      // CTAs that run at once, two an SM as far as clusters fit the GPCs (71 of 4 and 33 of 8 on B200)
+      const int64_t slots = static_cast<int64_t>(sp == 8 ? 264 : (sp == 4 ? 284 : 296)) * sms / 148;
+      const int64_t waves = (ctas + slots - 1) / slots;
+      const double share = ctas <= sms ? 1.0 : (waves == 1 ? 1.27 : 2.0);   // two CTAs share an SM's intake
+      const double block = (0.182 + 0.0818 * nt / 64) * share;
+      const double t = 4.8 + 0.118 * sp + 2.19 * nt / (64.0 * sp) +
+                       static_cast<double>(waves) * ((k_blocks + sp - 1) / sp * block + 0.527);
       if (t < lo) {
         lo = t;
         best = Plan{false, nt, sp};
