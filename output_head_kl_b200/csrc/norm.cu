@@ -531,11 +531,14 @@ cudaError_t grad_one(const NormGradParams& p, GradLaunch& g, cudaStream_t s) {
     warps = 65536 / ((a.numRegs + 7) / 8 * 8 * 32);
     if (dev < 64) reg_warps[dev].store(warps, std::memory_order_release);
   }
-  // The grid is the blocks that are resident at once: each runs its share of the rows to the end, and one
-  // block more would run alone after all others.
-  const int per_sm = std::min({kGradSmemMax / (g.smem + 2048), warps / (g.threads / 32), 2048 / g.threads});
-  g.grid = static_cast<int>(
-      std::min<int64_t>({g.rows, kNormGradBlocks, static_cast<int64_t>(g.sms) * std::max(1, per_sm)}));
+  // The grid is at most the blocks that are resident at once (each runs its share of the rows to the end, and
+  // one block more would run alone after all others), and no more than fill the rings' copies: beyond 512
+  // threads an SM (1024 with a row per warp) more rows in flight were slower (2880 columns: 23.5 us with two
+  // blocks an SM, 30.2 us with three).  A block gets two rows at least, which halves the partial sums.
+  const int most = (WARP ? 1024 : 512) / g.threads;
+  const int per_sm = std::min({kGradSmemMax / (g.smem + 2048), warps / (g.threads / 32), most});
+  g.grid = static_cast<int>(std::min<int64_t>(
+      {(g.rows + 1) / 2, kNormGradBlocks, static_cast<int64_t>(g.sms) * std::max(1, per_sm)}));
   const LaunchConfig cfg(dim3(g.grid), dim3(g.threads), g.smem, 0, s);
   return cudaLaunchKernelEx(&cfg.c, rmsnorm_grad_kernel<HF32, VPT, WARP>, p);
 }
