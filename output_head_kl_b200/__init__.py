@@ -28,6 +28,9 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "_lib", "libkdkl_debug.so")
 # The same library with per-role cycle counters in the GEMM kernels; see build.py.
 PROFILE_LIB_PATH = os.path.join(_HERE, "_lib", "libkdkl_prof.so")
 
+# Compiled argument marshalling of the latency-bound calls (csrc/binding.cpp).
+BINDING_PATH = os.path.join(_HERE, "_lib", "kdkl_binding.so")
+
 KDKL_OK = 0
 STATUS_NAMES = {0: "KDKL_OK", 1: "KDKL_ERR_NULL", 2: "KDKL_ERR_SHAPE", 3: "KDKL_ERR_ALIGN",
                 4: "KDKL_ERR_UNSUPPORTED", 5: "KDKL_ERR_WORKSPACE", 6: "KDKL_ERR_CUDA"}
@@ -155,6 +158,9 @@ def lib() -> ctypes.CDLL:
     L.kdkl_linear_backward.argtypes = [vp, vp, vp, vp, i64, i32, i32, ctypes.POINTER(LinearOptions), vp, vp, vp, vp,
                                        sz, vp]
     L.kdkl_linear_backward.restype = ctypes.c_int
+    # addresses of the entry points that the compiled marshalling calls
+    L.kdkl_addr = {n: ctypes.cast(getattr(L, "kdkl_" + n), vp).value
+                   for n in ("rmsnorm_forward", "rmsnorm_backward", "linear_forward", "linear_backward")}
     if hasattr(L, "kdkl_profile_read_role_cycles"):
         L.kdkl_profile_role_cycles_shape.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
         L.kdkl_profile_role_cycles_shape.restype = ctypes.c_int
@@ -383,6 +389,33 @@ def kdkl_count_valid(topk_idx, topk_logit, mask, tau, V, workspace, options=None
 
 
 # ---------------------------------------------------------------- operators ahead of the head
+# Each call first goes to the compiled marshalling, which checks the tensors and calls the library; where it
+# answers None (something is not as the call expects it), the Python path below checks again and raises.
+_binding = None
+
+
+def _fast():
+    """The compiled marshalling module (raises if it was not built)."""
+    global _binding
+    if _binding is None:
+        import importlib.machinery
+        import importlib.util
+        _import_torch()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"kdkl binding not built: {BINDING_PATH} is missing "
+                               "(run `python -m output_head_kl_b200.build`)")
+        loader = importlib.machinery.ExtensionFileLoader("kdkl_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("kdkl_binding", loader))
+        loader.exec_module(module)
+        _binding = module
+    return _binding
+
+
+def _handle(stream):
+    """A stream argument as the compiled marshalling takes it: a handle, or None for the current stream."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
+
+
 def _bad(status: int, where: str, detail: str):
     raise KDKLError(status, where, detail)
 
@@ -429,7 +462,13 @@ def kdkl_rmsnorm_forward(x, gamma, y, *, residual=None, h=None, y_scale=None, ep
 
     x [N, d] and residual / h (of one type, bf16 or fp32), gamma [d]; y bf16, or float8_e4m3fn with y_scale [N].
     """
+    st = (_binding or _fast()).rmsnorm_forward((_lib or lib()).kdkl_addr["rmsnorm_forward"], x, gamma, y, residual, h,
+                                               y_scale, float(eps), _handle(stream))
     fn = "kdkl_rmsnorm_forward"
+    if st is not None:
+        if check:
+            _check(st, fn)
+        return st
     torch, dev = _where(fn, x, "x")
     bf, f32 = torch.bfloat16, torch.float32
     N, d = shape = x.shape
@@ -452,7 +491,13 @@ def kdkl_rmsnorm_workspace_bytes(N: int, d: int) -> int:
 
 def kdkl_rmsnorm_backward(dy, h, gamma, dx, dgamma, workspace, *, dh=None, eps=1e-6, stream=None, check=True) -> int:
     """Calls kdkl_rmsnorm_backward: dx (the gradient of x and residual alike, plus dh) and dgamma."""
+    st = (_binding or _fast()).rmsnorm_backward((_lib or lib()).kdkl_addr["rmsnorm_backward"], dy, h, gamma, dx, dgamma,
+                                                workspace, dh, float(eps), _handle(stream))
     fn = "kdkl_rmsnorm_backward"
+    if st is not None:
+        if check:
+            _check(st, fn)
+        return st
     torch, dev = _where(fn, h, "h")
     bf, f32 = torch.bfloat16, torch.float32
     N, d = shape = h.shape
@@ -495,7 +540,14 @@ def kdkl_linear_forward(x, W, y, workspace, *, bias=None, residual=None, pre=Non
 
     x [M, d_in] and W [d_out, d_in] both bf16, or both float8_e4m3fn with x_scale [M] and w_scale [d_out].
     """
+    st = (_binding or _fast()).linear_forward((_lib or lib()).kdkl_addr["linear_forward"], x, W, y, workspace, bias,
+                                              residual, pre, ACTIVATIONS.get(activation, activation), x_scale, w_scale,
+                                              plan, _handle(stream))
     fn = "kdkl_linear_forward"
+    if st is not None:
+        if check:
+            _check(st, fn)
+        return st
     torch, dev = _where(fn, x, "x")
     bf, f32 = (torch.bfloat16,), (torch.float32,)
     M, d_in = x.shape
@@ -521,7 +573,14 @@ def kdkl_linear_backward(dy, x, W, dx, dW, workspace, *, pre=None, dbias=None, a
 
     dx, dW and dbias may each be None; the gradient of the forward's residual is dy itself.
     """
+    st = (_binding or _fast()).linear_backward((_lib or lib()).kdkl_addr["linear_backward"], dy, x, W, dx, dW, workspace,
+                                               pre, dbias, ACTIVATIONS.get(activation, activation), dx_plan, dw_plan,
+                                               _handle(stream))
     fn = "kdkl_linear_backward"
+    if st is not None:
+        if check:
+            _check(st, fn)
+        return st
     torch, dev = _where(fn, dy, "dy")
     bf = (torch.bfloat16,)
     M, d_out = out = dy.shape

@@ -28,6 +28,8 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libkdkl.so")
 DEBUG_LIB = os.path.join(OUT_DIR, "libkdkl_debug.so")
 PROFILE_LIB = os.path.join(OUT_DIR, "libkdkl_prof.so")
+# Tensor checks and argument lists of the latency-bound calls, compiled against torch's headers.
+BINDING = os.path.join(OUT_DIR, "kdkl_binding.so")
 SOURCES = ("kernels.cu", "api.cu", "noalloc.cu", "norm.cu", "linear.cu", "layer_api.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -75,10 +77,30 @@ def _build_one(lib: str, prefix: str, defines, log_name: str):
     return logs
 
 
+def _build_binding():
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    libs = library_paths()
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], *[a for d in include_paths() for a in ("-isystem", d)],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           os.path.join(CSRC, "binding.cpp"), *[a for d in libs for a in ("-L", d, f"-Wl,-rpath,{d}")],
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", BINDING + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True, profile: bool = True) -> str:
-    """Builds libkdkl.so (and, when asked, the bounds-checking libkdkl_debug.so and the
+    """Builds libkdkl.so and its binding (and, when asked, the bounds-checking libkdkl_debug.so and the
     cycle-counting libkdkl_prof.so)."""
     os.makedirs(OUT_DIR, exist_ok=True)
+    if force or _stale(BINDING):
+        _build_binding()
     if force or _stale(LIB):
         logs = _build_one(LIB, "", [], "ptxas.log")
         if verbose:

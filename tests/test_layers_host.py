@@ -159,3 +159,25 @@ def test_binding_refuses_tensors_off_the_device():
         K.kdkl_linear_backward(x, x, x, x, x, x)
     with pytest.raises(K.KDKLError, match="3 dimensions"):
         K.kdkl_rmsnorm_forward(x[None], x[0], x)
+
+
+def test_binding_missing_fails_loudly(monkeypatch, tmp_path):
+    monkeypatch.setattr(K, "_binding", None)
+    monkeypatch.setattr(K, "BINDING_PATH", str(tmp_path / "nope.so"))
+    x = torch.zeros(4, 16, dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="not built"):
+        K.kdkl_rmsnorm_forward(x, x[0], x)
+
+
+def test_compiled_marshalling_declines_what_it_does_not_take():
+    """None (and no crash) for arguments that are no tensors, off the device, or of the wrong kind; the Python
+    path then raises, naming the argument."""
+    b, x = K._fast(), torch.zeros(4, 16, dtype=torch.bfloat16)
+    for bad in (x, None, 3, "x", torch.zeros(4, 16).to_sparse(), object()):
+        assert b.rmsnorm_forward(0, bad, x[0], x, None, None, None, 1e-6, None) is None
+        assert b.rmsnorm_backward(0, bad, bad, x[0], x, x[0], x, None, 1e-6, None) is None
+        assert b.linear_forward(0, bad, x, x, x, None, None, None, 0, None, None, 0, None) is None
+        assert b.linear_backward(0, bad, x, x, x, x, x, None, None, 0, 0, 0, None) is None
+    with pytest.raises(TypeError):
+        b.linear_forward(0, x)
+    assert ctypes.cast(K.lib().kdkl_linear_forward, ctypes.c_void_p).value == K.lib().kdkl_addr["linear_forward"]
