@@ -327,7 +327,7 @@ kdkl_status kdkl_teacher_topk(const void* hidden, const void* W, int64_t N, int3
  * Same conventions as above: dense row-major tensors of the current device,
  * caller-owned workspaces, asynchronous on `stream`, host checks before any
  * launch, results that repeat bit for bit; every call can be captured in a CUDA
- * graph after one eager call.  Every row takes part: rows of padding hold finite
+ * graph after one eager call.  Tensors without rows (N or M = 0) may be NULL.  Every row takes part: rows of padding hold finite
  * values (a NaN or infinity in a row spreads to that row's outputs, and in a
  * gradient to the column sums and weight gradients that the row enters).
  * ---------------------------------------------------------------------------

@@ -55,19 +55,20 @@ int64_t tail_tiles(int64_t tiles, int sms) { return tiles % (sms / 2); }
 // left over (B200, 148 SMs: 33 and 15 were found resident; one less is counted on).
 int64_t cluster_slots(int sms, int ctas) { return static_cast<int64_t>(ctas == 4 ? 32 : 14) * sms / 148; }
 
+// Whether a product's tiles, if they are split, are split by clusters, without the workspace: those of fewer
+// tiles than a wave (of a B200's 74 pairs; on any device, so that the workspace's size does not depend on it).
+constexpr int kWaveTiles = 74;
+bool split_by_cluster(LinOp op, int64_t tiles) { return op != kLinDw && tiles < kWaveTiles; }
+
 // Whether the tiles of the last wave can each be split into `sp` shares of the reduction: all shares run at
 // once and keep at least four reduction blocks.  Where there is no full wave, a cluster of 2 or 4 pairs shares
 // each tile (dW: any number of shares, by way of the workspace, as after full waves).
 bool can_split(LinOp op, int64_t tiles, int k_blocks, int sms, int sp) {
   const int64_t tail = tail_tiles(tiles, sms);
   if (sp < 2 || sp > kMaxTailSplits || tail == 0 || k_blocks / sp < 4) return false;
-  if (tail * sp > std::min<int64_t>(sms / 2, kMaxShares)) return false;
-  if (op == kLinDw || tail < tiles) return true;
-  return (sp == 2 || sp == 4) && tiles <= cluster_slots(sms, 2 * sp);
+  if (split_by_cluster(op, tiles)) return (sp == 2 || sp == 4) && tiles <= cluster_slots(sms, 2 * sp);
+  return tail * sp <= std::min<int64_t>(sms / 2, kMaxShares);
 }
-
-// Splits by clusters, without the workspace.
-bool cluster_split(LinOp op, int64_t tiles, int sms, int sp) { return sp > 1 && op != kLinDw && tiles < sms / 2; }
 
 // Product out[rows, cols] with `k_blocks` reduction blocks.
 //
@@ -93,7 +94,7 @@ Plan plan_linear(LinOp op, int64_t rows, int64_t cols, int k_blocks, int sms) {
       if (sp > 1 && !can_split(op, tiles, k_blocks, sms, sp)) continue;
       double t = 3.26 + 5.72 * width + static_cast<double>(full) * (k_blocks * kb + 0.441 * width);
       if (tail) t += (k_blocks + sp - 1) / sp * kb + (full ? 0.441 * width : 0.0);
-      if (sp > 1) t += cluster_split(op, tiles, sms, sp) ? 1.85 - 3.13 * width : 9.74 + 0.488 * sp;
+      if (sp > 1) t += split_by_cluster(op, tiles) ? 1.85 - 3.13 * width : 9.74 + 0.488 * sp;
       if (t < lo) {
         lo = t;
         best = Plan{true, bn, sp};
@@ -170,7 +171,8 @@ struct LinearLayout {
 
 // Bytes of the partial sums that a product out[rows, cols] may split its last wave into, whatever its tile
 // width (narrower tiles are more, but smaller).
-size_t share_bytes(int64_t rows, int64_t cols) {
+size_t share_bytes(LinOp op, int64_t rows, int64_t cols) {
+  if (split_by_cluster(op, ((rows + 255) / 256) * ((cols + 127) / 128))) return 0;
   const int64_t tiles = ((rows + 255) / 256) * ((cols + 255) / 256);
   return static_cast<size_t>(std::min<int64_t>(kMaxShares, tiles * kMaxTailSplits)) * kShareBytes;
 }
@@ -183,8 +185,8 @@ LinearLayout linear_layout(int64_t M, int32_t d_in, int32_t d_out, bool backward
   L.tickets = kFlagBytes;
   L.col_tickets = L.tickets + kTicketBytes;
   L.shares = align_up(L.col_tickets + (backward ? static_cast<size_t>((d_out + 255) / 256) * 4 : 0), 256);
-  size_t off = L.shares + (backward ? std::max(share_bytes(M, d_in), share_bytes(d_out, d_in))
-                                    : share_bytes(M, d_out));
+  size_t off = L.shares + (backward ? std::max(share_bytes(kLinDx, M, d_in), share_bytes(kLinDw, d_out, d_in))
+                                    : share_bytes(kLinFwd, M, d_out));
   if (backward) {
     L.dz = off;
     off = align_up(off + static_cast<size_t>(M) * d_out * 2, 256);
@@ -230,7 +232,7 @@ cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b
     if ((p.pre && !box(&m.pre, p.pre)) || (p.residual && !box(&m.res, p.residual))) return cudaErrorInvalidValue;
     p.n_tiles = static_cast<int>((cols + bn - 1) / bn);
     p.tiles = static_cast<int>((rows + 255) / 256) * p.n_tiles;
-    if (cluster_split(op, p.tiles, sms, plan.splits)) return launch_linear_split(op, bn, m, p, s);
+    if (plan.splits > 1 && split_by_cluster(op, p.tiles)) return launch_linear_split(op, bn, m, p, s);
     const int tail = plan.splits > 1 ? static_cast<int>(tail_tiles(p.tiles, sms)) : 0;
     p.full_units = p.tiles - tail;
     p.units = p.full_units + tail * plan.splits;
@@ -306,8 +308,8 @@ kdkl_status kdkl_rmsnorm_forward(const void* x, const void* residual, const void
   if (st != KDKL_OK) return st;
   if (!float_dtype(x_dtype)) return fail(KDKL_ERR_UNSUPPORTED, "x must be KDKL_BF16 or KDKL_F32");
   if (y_dtype != KDKL_BF16 && y_dtype != KDKL_E4M3) return fail(KDKL_ERR_UNSUPPORTED, "y must be KDKL_BF16 or KDKL_E4M3");
-  if (!x || !gamma || !y) return fail(KDKL_ERR_NULL, "x, gamma and y must be non-NULL");
-  if ((y_dtype == KDKL_E4M3) != (y_scale != nullptr))
+  if (!gamma || (N > 0 && (!x || !y))) return fail(KDKL_ERR_NULL, "x, gamma and y must be non-NULL");
+  if (N > 0 && (y_dtype == KDKL_E4M3) != (y_scale != nullptr))
     return fail(KDKL_ERR_NULL, "y_scale goes with a KDKL_E4M3 y, and only with one");
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(h, 16) || !aligned(y, 16))
     return fail(KDKL_ERR_ALIGN, "x, residual, gamma, h and y must be 16-byte aligned");
@@ -345,7 +347,7 @@ kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gam
                                   float* dgamma, void* workspace, size_t workspace_bytes, void* stream) {
   kdkl_status st = check_norm(N, d, eps, h_dtype, gamma_dtype);
   if (st != KDKL_OK) return st;
-  if (!dy || !h || !gamma || !dx || !dgamma || !workspace)
+  if (!gamma || !dgamma || !workspace || (N > 0 && (!dy || !h || !dx)))
     return fail(KDKL_ERR_NULL, "dy, h, gamma, dx, dgamma and workspace must be non-NULL");
   if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(gamma, 16) || !aligned(dh, 16) || !aligned(dx, 16))
     return fail(KDKL_ERR_ALIGN, "dy, h, gamma, dh and dx must be 16-byte aligned");
@@ -425,9 +427,10 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   kdkl_status st = check_linear_shape(M, d_in, d_out, o.operands);
   if (st != KDKL_OK) return st;
   if ((st = check_activation(o.activation)) != KDKL_OK) return st;
-  if (!x || !W || !y || !workspace) return fail(KDKL_ERR_NULL, "x, W, y and workspace must be non-NULL");
+  if (!W || !workspace || (M > 0 && (!x || !y)))
+    return fail(KDKL_ERR_NULL, "x, W, y and workspace must be non-NULL");
   const bool f8 = o.operands == KDKL_E4M3;
-  if (f8 && (!o.x_scale || !o.w_scale)) return fail(KDKL_ERR_NULL, "KDKL_E4M3 operands need x_scale and w_scale");
+  if (f8 && (!o.w_scale || (M > 0 && !o.x_scale))) return fail(KDKL_ERR_NULL, "KDKL_E4M3 operands need x_scale and w_scale");
   if (!f8 && (o.x_scale || o.w_scale)) return fail(KDKL_ERR_UNSUPPORTED, "x_scale and w_scale go with KDKL_E4M3 operands only");
   if (!aligned(x, 16) || !aligned(W, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) ||
       !aligned(pre, 16))
@@ -445,7 +448,7 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t tiles = plan.pair ? ((M + 255) / 256) * ((d_out + plan.tile - 1) / plan.tile) : 0;
   const bool clear_ahead =
-      kClearAhead || M == 0 || (plan.pair && plan.splits > 1 && !cluster_split(op, tiles, dv.sms, plan.splits));
+      kClearAhead || M == 0 || (plan.pair && plan.splits > 1 && !split_by_cluster(op, tiles));
   if (clear_ahead && (st = clear_header(workspace, L, s)) != KDKL_OK) return st;
   if (M == 0) return ok();
   LinParams p = {};
@@ -473,12 +476,12 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   if (st != KDKL_OK) return st;
   if (o.operands != KDKL_BF16) return fail(KDKL_ERR_UNSUPPORTED, "KDKL_E4M3 operands have no gradient");
   if ((st = check_activation(o.activation)) != KDKL_OK) return st;
-  if (!dx && !dW && !dbias) return fail(KDKL_ERR_NULL, "one of dx, dW and dbias must be non-NULL");
-  if (!dy || !workspace) return fail(KDKL_ERR_NULL, "dy and workspace must be non-NULL");
+  if (M > 0 && !dx && !dW && !dbias) return fail(KDKL_ERR_NULL, "one of dx, dW and dbias must be non-NULL");
+  if (!workspace || (M > 0 && !dy)) return fail(KDKL_ERR_NULL, "dy and workspace must be non-NULL");
   if (dx && !W) return fail(KDKL_ERR_NULL, "dx needs W");
-  if (dW && !x) return fail(KDKL_ERR_NULL, "dW needs x");
+  if (M > 0 && dW && !x) return fail(KDKL_ERR_NULL, "dW needs x");
   const bool act = o.activation != KDKL_ACT_NONE;
-  if (act && !pre) return fail(KDKL_ERR_NULL, "the activation's gradient needs pre");
+  if (M > 0 && act && !pre) return fail(KDKL_ERR_NULL, "the activation's gradient needs pre");
   if (!aligned(dy, 16) || !aligned(pre, 16) || !aligned(x, 16) || !aligned(W, 16) || !aligned(dx, 16) ||
       !aligned(dW, 16))
     return fail(KDKL_ERR_ALIGN, "dy, pre, x, W, dx and dW must be 16-byte aligned");

@@ -3,10 +3,12 @@
 //   forward   z = x W^T + b,  y = act(z) + r           x [M, d_in], W [d_out, d_in], y [M, d_out]
 //   gradient  dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_rows dz
 //
-// Two tcgen05 kernels share the operand layouts (128-byte swizzled tiles fetched by TMA):
+// Three tcgen05 kernels share the operand layouts (128-byte swizzled tiles fetched by TMA):
 //
 //   linear_pair_kernel   256 x BN output tiles by CTA pairs (cta_group::2), persistent, two accumulators
 //                        in TMEM so that the epilogue of one tile runs under the next tile's MMAs.
+//   linear_split_kernel  the same tiles, fewer than there are pairs: 2 or 4 pairs of a cluster share a tile's
+//                        reduction and join over distributed shared memory.
 //   linear_small_kernel  few rows: the operands swap roles, so that 128 rows of W fill the MMA's M and the
 //                        rows of x its N (16 to 128), and a cluster of CTAs splits the reduction and joins
 //                        the partial tiles over distributed shared memory in a fixed order.  The weights
@@ -323,6 +325,11 @@ struct Finisher {
 // Warp 0 issues the TMA loads, warp 1 of the even CTA the MMAs, and eight epilogue warps read TMEM (two
 // per 32-lane quarter, each half of the tile's columns).  Tiles are swept in groups of row_group row
 // blocks, column by column, so that the pairs running at once share their A rows and B columns in L2.
+//
+// Bound by the tensor cores and, equally, by what an SM takes in from L2: a 64-wide reduction block of a 256 x 256
+// tile is 512 cycles of MMA and 32 KB a CTA, 64 bytes a cycle.  Measured at 16384 x 4096 x 4096 under the power cap:
+// plain product 403-415 us (cuBLAS 402-405), with SiLU, residual and z stored 461-473; dx 409, dW 433 (the last
+// wave split: 459 without).  An epilogue of one tile takes 4,000 (plain) to 10,700 cycles (everything).
 // ============================================================================
 constexpr int kPairThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -681,7 +688,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // share of the reduction blocks of one tile, spills it to its shared memory over the drained operand stages
 // ([32-column chunk][4 columns][row], so that both ways move consecutive 16-byte groups), and after a cluster
 // barrier each CTA joins and finishes BN / splits columns of its 128 rows, adding the shares in pair order.
-// The epilogue is shared out with the join, so splitting costs no more than it saves there.
+// The epilogue is shared out with the join, so splitting costs no more than it saves there: 512 x 4096 x 4096 in
+// 19.9 us against 26.4 us unsplit.
 // ============================================================================
 template <int OP, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -884,7 +892,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // A = 128 rows of W (for dx: 128 columns of W, MN-major), B = NT rows of x (or dz).  Each CTA reduces its
 // share of the reduction blocks into a [128 x NT] TMEM tile, spills it to shared memory as [row][column]
 // fp32, and after a cluster barrier each CTA joins and finishes 1 / splits of the tile: for every output it
-// adds the partial sums in CTA order.  No workspace, no atomics, one launch.
+// adds the partial sums in CTA order.  No workspace, no atomics, one launch.  Bound by HBM while the weights stream
+// (1 x 4096 x 4096: 9,300 of 16,600 cycles), else by set-up, the first bytes' latency and the join; 10.2 us back to
+// back, e4m3 7.2 us.
 // ============================================================================
 constexpr int kSmallThreads = 192;
 constexpr int kMaxSplits = 8;

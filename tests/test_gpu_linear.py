@@ -323,6 +323,14 @@ def test_empty_batch():
                                     ws.numel(), s) == 0
     torch.cuda.synchronize()
     assert bool((buf == 5).all()) and bool((dW == 0).all()) and bool((db == 0).all())
+    # empty tensors, which torch gives no address, through the binding
+    e, dW[:], db[:] = torch.empty(0, 64, dtype=BF, device="cuda"), 5, 5
+    K.kdkl_linear_forward(e, W, e, ws, bias=W[0], residual=e, pre=e, activation="silu")
+    K.kdkl_linear_backward(e, e, W, e, dW, ws, pre=e, dbias=db, activation="silu")
+    torch.cuda.synchronize()
+    assert bool((dW == 0).all()) and bool((db == 0).all())
+    e8, s8 = e.to(F8), torch.empty(0, device="cuda")
+    K.kdkl_linear_forward(e8, W.to(F8), e, ws, x_scale=s8, w_scale=torch.ones(64, device="cuda"))
 
 
 def test_binding_refusals():

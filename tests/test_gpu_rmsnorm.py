@@ -221,7 +221,6 @@ def test_empty_batch():
     gamma = torch.ones(64, dtype=BF, device="cuda")
     dg = torch.full((64,), 3.0, device="cuda")
     ws = torch.empty(K.kdkl_rmsnorm_workspace_bytes(0, 64), dtype=torch.uint8, device="cuda")
-    # torch gives empty tensors a null address, which the library refuses: pass rows of another buffer
     buf = torch.full((1, 64), 5.0, dtype=BF, device="cuda")
     lib = K.lib()
     s = torch.cuda.current_stream().cuda_stream
@@ -230,7 +229,14 @@ def test_empty_batch():
     assert lib.kdkl_rmsnorm_backward(buf.data_ptr(), buf.data_ptr(), gamma.data_ptr(), None, 0, 64, EPS, 0, 0,
                                      buf.data_ptr(), dg.data_ptr(), ws.data_ptr(), ws.numel(), s) == 0
     torch.cuda.synchronize()
-    assert bool((buf == 5).all()) and bool((dg == 0).all()) and e.numel() == 0
+    assert bool((buf == 5).all()) and bool((dg == 0).all())
+    # empty tensors, which torch gives no address, through the binding
+    dg.fill_(3)
+    K.kdkl_rmsnorm_forward(e, gamma, e, residual=e, h=e)
+    K.kdkl_rmsnorm_forward(e, gamma, e.to(F8), y_scale=torch.empty(0, device="cuda"))
+    K.kdkl_rmsnorm_backward(e, e, gamma, e, dg, ws, dh=e)
+    torch.cuda.synchronize()
+    assert bool((dg == 0).all())
 
 
 def test_binding_refusals():
