@@ -94,43 +94,47 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Sum (or NaN-keeping maximum) over the row's threads: a warp, or a block of `warps` warps that
-// exchange through `slot` (one barrier; the caller alternates slots, so that a slot is rewritten
-// only after a later barrier).
-template <bool WARP, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* slot, int warps) {
+// Sum and, with Q, NaN-keeping maximum over the row's threads, with one exchange: a warp, or a block of `warps`
+// warps through `slots`.
+template <bool WARP, bool Q>
+__device__ __forceinline__ void row_reduce(float& sum, float& top, float2* slots, int warps) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? max_nan(v, w) : v + w;
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (Q) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  if (WARP) return v;
+  if (WARP) return;
   const int lane = threadIdx.x & 31;
-  if (lane == 0) slot[threadIdx.x >> 5] = v;
+  if (lane == 0) slots[threadIdx.x >> 5] = make_float2(sum, top);
   __syncthreads();
   // every thread reduces the same values in the same order: reading them is cheapest for a few warps, another
   // round of shuffles the shorter chain for many (2.1 against 2.4 us for one row of 4096)
   if (warps <= 8) {
-    v = slot[0];
-    for (int w = 1; w < warps; ++w) v = MAX ? max_nan(v, slot[w]) : v + slot[w];
-    return v;
+    sum = slots[0].x;
+    top = slots[0].y;
+    for (int w = 1; w < warps; ++w) {
+      sum += slots[w].x;
+      if (Q) top = max_nan(top, slots[w].y);
+    }
+    return;
   }
-  v = lane < warps ? slot[lane] : 0.f;
+  const float2 mine = lane < warps ? slots[lane] : make_float2(0.f, 0.f);
+  sum = mine.x;
+  top = mine.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? max_nan(v, w) : v + w;
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (Q) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  return v;
 }
 
 // One row per warp (WARP: four rows a block, d <= 256 VPT) or per block.  A thread holds VPT steps of
 // kV elements.  Nothing is kept between rows, so the grid is one block per row (or four rows): the
 // next block's loads cover this one's barrier.  Measured (x and y bf16): 32768 x 4096 in 156 us, 6.9 TB/s;
-// 65536 x 1024 in 81 us, 6.6 TB/s; e4m3 output 145 us, 6.5 TB/s; one row of 4096 in 1.9 us.
+// 65536 x 1024 in 81 us, 6.6 TB/s; e4m3 output 139 us, 6.8 TB/s; one row of 4096 in 1.8 us.
 template <bool XF32, bool HF32, bool Q, int VPT, bool WARP>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormParams p) {
-  __shared__ float s_red[2][32];
+  __shared__ float2 s_red[32];
   const int lane_t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int row_threads = WARP ? 32 : blockDim.x;
   const int warps = blockDim.x >> 5;
@@ -177,26 +181,37 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
       load_gamma(p.gamma, p.gamma_f32, c, gm[i]);
     }
   }
-  ss = row_reduce<WARP, false>(ss, s_red[0], warps);
-  const float r = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+  // e4m3: q = y / scale does not depend on r, so the row's largest |h gamma| is found with the sum of squares
   float top = 0.f;
+  if (Q) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * row_threads + lane_t) * kV;
-    if (c < p.d) {
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * row_threads + lane_t) * kV;
+      if (c < p.d) {
 #pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        v[i][j] = v[i][j] * r * gm[i][j];
-        if (Q) top = max_nan(top, fabsf(v[i][j]));
+        for (int j = 0; j < kV; ++j) {
+          v[i][j] *= gm[i][j];
+          top = max_nan(top, fabsf(v[i][j]));
+        }
       }
-      if (!Q) Pack<false>::store(p.y, base + c, v[i]);
     }
   }
-  if (Q) {
-    top = row_reduce<WARP, true>(top, s_red[1], warps);
-    if (lane_t == 0) p.y_scale[n] = top / kE4m3Max;
-    // q = y * (448 / top); a row of zeros has scale 0 and q = 0, and a row so small that 448 / top would
-    // overflow is first multiplied by a power of two, which is exact
+  row_reduce<WARP, Q>(ss, top, s_red, warps);
+  const float r = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+  if (!Q) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * row_threads + lane_t) * kV;
+      if (c < p.d) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[i][j] = v[i][j] * r * gm[i][j];
+        Pack<false>::store(p.y, base + c, v[i]);
+      }
+    }
+  } else {
+    if (lane_t == 0) p.y_scale[n] = top * r / kE4m3Max;
+    // q = h gamma (448 / top); a row of zeros (or whose squares overflow: y = 0) has scale 0 and q = 0, and a row
+    // so small that 448 / top would overflow is first multiplied by a power of two, which is exact
     if (top < 1e-30f) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormPara
         for (int j = 0; j < kV; ++j) v[i][j] *= 0x1p100f;
       top *= 0x1p100f;
     }
-    const float inv = top == 0.f ? 0.f : kE4m3Max / top;
+    const float inv = (top == 0.f || (r == 0.f && top < INFINITY)) ? 0.f : kE4m3Max / top;
     uint8_t* out = static_cast<uint8_t*>(p.y);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -466,8 +481,8 @@ NormShape warp_shape(int vecs) {
 
 // Forward.  Up to 1024 elements and with rows enough, a warp per row: no barrier.  Above, with few rows the
 // fewest steps (the shortest chain of loads), else blocks of 256 threads, so that more rows are in flight per
-// SM; with an e4m3 output, whose second reduction makes each row's fixed cost twice as large, four steps from
-// 4096 elements on (142 against 165 us for 32768 x 4096).
+// SM; with an e4m3 output four steps from 4096 elements on (32768 x 4096 with an fp32 stream: 213 against 232 us
+// with two steps; with a bf16 stream both take 138 us).
 NormShape norm_shape(int64_t N, int d, bool e4m3, int sms) {
   const int vecs = (d + kV - 1) / kV;
   if (vecs <= 32 * 4 && N >= sms) return warp_shape(vecs);
@@ -477,16 +492,24 @@ NormShape norm_shape(int64_t N, int d, bool e4m3, int sms) {
 
 // Gradient.  Two steps a thread wherever they hold the row (a warp per row up to 512 elements, with rows
 // enough): a row's fixed cost is shared by 16 elements, and the ring of the next rows fits beside it.
-NormShape norm_grad_shape(int64_t N, int d, int sms) {
+int grad_threads(int vecs) {   // of rows that are read twice
+  const int vpt = vecs > 4 * kNormMaxThreads ? 8 : 4;
+  return ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
+}
+
+NormShape norm_grad_shape(int64_t N, int d, bool h_f32, int sms) {
   const int vecs = (d + kV - 1) / kV;
   if (vecs <= 64 && N >= 8 * static_cast<int64_t>(sms)) return warp_shape(vecs);
-  if (vecs > 1024) return block_shape(vecs, kNormMaxThreads);
+  // two steps of 512 threads, of 480 with an fp32 stream: a larger ring does not fit shared memory
+  if (vecs > (h_f32 ? 960 : 1024)) return {false, vecs > 4 * kNormMaxThreads ? 8 : 4, grad_threads(vecs)};
   return {false, 2, std::max(32, (vecs + 63) / 64 * 32)};
 }
 
 constexpr int kNormWarps = 4;       // rows of a block with a row per warp
 constexpr int kNormGradWarps = 4;
 constexpr int kGradSmemMax = 226 * 1024;
+static_assert(kGradStages * grad_pieces(2, false) * 512 * 16 <= kGradSmemMax, "the ring of 512 threads, bf16");
+static_assert(kGradStages * grad_pieces(2, true) * 480 * 16 <= kGradSmemMax, "the ring of 480 threads, fp32");
 
 template <bool XF32, bool HF32, bool Q>
 cudaError_t launch_norm(const NormParams& p, const NormShape& sh, cudaStream_t s) {
@@ -573,7 +596,7 @@ cudaError_t launch_rmsnorm(const NormParams& p, int sms, cudaStream_t s) {
 
 int launch_rmsnorm_grad(const NormGradParams& p, int sms, cudaStream_t s, cudaError_t* err) {
   GradLaunch g;
-  g.sh = norm_grad_shape(p.N, p.d, sms);
+  g.sh = norm_grad_shape(p.N, p.d, p.h_f32, sms);
   g.threads = g.sh.warp ? 32 * kNormGradWarps : g.sh.threads;
   g.smem = (grad_ring(g.sh.vpt) ? kGradStages * grad_pieces(g.sh.vpt, p.h_f32) * g.threads * 16 : 0) +
            (g.sh.warp ? (kNormGradWarps - 1) * p.d * 4 : 0);

@@ -171,7 +171,8 @@ def test_backward(N, d):
 
 
 @pytest.mark.parametrize("ht,gt", [(F32, F32), (F32, BF), (BF, F32)])
-@pytest.mark.parametrize("N,d", [(1003, 896), (161, 2880), (2000, 72)])
+@pytest.mark.parametrize("N,d", [(1003, 896), (161, 2880), (2000, 72), (40, 7680), (40, 7688), (3, 8192), (70, 8200),
+                                 (5, 16392), (2, 32768)])
 def test_backward_types(N, d, ht, gt):
     h, dh, gamma = _data(N, d, ht, ht, gt, seed=11)
     dy = torch.randn(N, d, device="cuda").to(BF)
