@@ -217,6 +217,27 @@ def test_backward_in_place_and_repeatable():
         assert torch.equal(acc, dx) and torch.equal(dg3, dg)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows land where they belong (all others are zero)."""
+    N, d, last = 262300, 8192, 40
+    free, _ = torch.cuda.mem_get_info()
+    assert N * d > 2 ** 31 and free > 24 << 30
+    h, dh, gamma = _data(last, d, BF, BF, BF, seed=15)
+    dy = torch.randn(last, d, device="cuda").to(BF)
+    big = [torch.zeros(N, d, dtype=BF, device="cuda") for _ in range(3)]
+    big[0][-last:], big[1][-last:] = h, dy
+    K.kdkl_rmsnorm_forward(big[0], gamma, big[2], eps=EPS)
+    _, want, _ = _forward(h, None, gamma, BF, with_h=False)
+    assert torch.equal(big[2][-last:], want) and not bool(big[2][:-last].any())
+    dg = torch.empty(d, device="cuda")
+    ws = torch.empty(K.kdkl_rmsnorm_workspace_bytes(N, d), dtype=torch.uint8, device="cuda")
+    K.kdkl_rmsnorm_backward(big[1], big[0], gamma, big[2], dg, ws, eps=EPS)
+    dx, dgw = _grad(dy, h, gamma, None)
+    assert torch.equal(big[2][-last:], dx) and not bool(big[2][:-last].any())
+    scale = (dy.float().abs() * h.float().abs()).sum(0) / h.float().square().mean(1).sqrt().min()
+    assert bool(((dg - dgw).abs() <= 256 * U * scale).all())      # the same terms in another order
+
+
 def test_empty_batch():
     e = torch.empty(0, 64, dtype=BF, device="cuda")
     gamma = torch.ones(64, dtype=BF, device="cuda")
