@@ -15,11 +15,10 @@ namespace {
 
 constexpr int32_t kMaxWidth = 1 << 20;
 constexpr size_t kFlagBytes = 256;
-// Shares of split tiles that a launch of large tiles may have (a wave of CTA pairs has 74 on B200), their
-// partial sums (256 x 256 fp32 each at most) and the tickets of their tiles.
+// Shares of split tiles that a launch of large tiles may have (a wave of CTA pairs has 74 on B200; each leaves
+// 256 x bn fp32 partial sums), and the tickets of their tiles.
 constexpr int kMaxShares = 80;
 constexpr int kMaxTailSplits = 8;
-constexpr size_t kShareBytes = 256 * 256 * 4;
 constexpr size_t kTicketBytes = kMaxShares / 2 * kTileTickets * 4;
 
 bool float_dtype(int32_t t) { return t == KDKL_BF16 || t == KDKL_F32; }
@@ -166,15 +165,21 @@ kdkl_linear_options default_linear_options() {
 }
 
 struct LinearLayout {
-  size_t tickets = 0, col_tickets = 0, shares = 0, dz = 0, part = 0, total = 0;
+  size_t tickets = 0, col_tickets = 0, shares = 0, share_bytes = 0, dz = 0, part = 0, total = 0;
 };
 
-// Bytes of the partial sums that a product out[rows, cols] may split its last wave into, whatever its tile
-// width (narrower tiles are more, but smaller).
+// Bytes of the partial sums that a product out[rows, cols] may split its last wave into: the most of any tile
+// width.  Neither the narrowest nor the widest tiles need the most everywhere: 385 to 512 columns are two tiles of
+// 256 but three of 192, whose shares are larger in all.
 size_t share_bytes(LinOp op, int64_t rows, int64_t cols) {
-  if (split_by_cluster(op, ((rows + 255) / 256) * ((cols + 127) / 128))) return 0;
-  const int64_t tiles = ((rows + 255) / 256) * ((cols + 255) / 256);
-  return static_cast<size_t>(std::min<int64_t>(kMaxShares, tiles * kMaxTailSplits)) * kShareBytes;
+  size_t most = 0;
+  for (int bn : {256, 192, 128}) {
+    const int64_t tiles = ((rows + 255) / 256) * ((cols + bn - 1) / bn);
+    if (split_by_cluster(op, tiles)) continue;
+    const int64_t shares = std::min<int64_t>(kMaxShares, tiles * kMaxTailSplits);   // as can_split allows
+    most = std::max(most, static_cast<size_t>(shares) * 256 * bn * 4);
+  }
+  return most;
 }
 
 // Workspace: the flag word and the tickets (everything before `shares` is cleared ahead of the launches that
@@ -185,8 +190,9 @@ LinearLayout linear_layout(int64_t M, int32_t d_in, int32_t d_out, bool backward
   L.tickets = kFlagBytes;
   L.col_tickets = L.tickets + kTicketBytes;
   L.shares = align_up(L.col_tickets + (backward ? static_cast<size_t>((d_out + 255) / 256) * 4 : 0), 256);
-  size_t off = L.shares + (backward ? std::max(share_bytes(kLinDx, M, d_in), share_bytes(kLinDw, d_out, d_in))
-                                    : share_bytes(kLinFwd, M, d_out));
+  L.share_bytes = backward ? std::max(share_bytes(kLinDx, M, d_in), share_bytes(kLinDw, d_out, d_in))
+                           : share_bytes(kLinFwd, M, d_out);
+  size_t off = L.shares + L.share_bytes;
   if (backward) {
     L.dz = off;
     off = align_up(off + static_cast<size_t>(M) * d_out * 2, 256);
@@ -236,6 +242,7 @@ cudaError_t run_product(LinOp op, const Plan& plan, const void* a, const void* b
     const int tail = plan.splits > 1 ? static_cast<int>(tail_tiles(p.tiles, sms)) : 0;
     p.full_units = p.tiles - tail;
     p.units = p.full_units + tail * plan.splits;
+    if (static_cast<int64_t>(tail) * plan.splits * 256 * bn > p.part_floats) return cudaErrorInvalidValue;
     // When B (the weights, or x for dW) stays in L2, two row blocks at a time read A once while it is
     // hot: 412 against 424 us for 16384 x 4096 x 4096 at a steady clock; a B beyond L2 is swept for
     // eight row blocks at a time.
@@ -463,6 +470,7 @@ kdkl_status kdkl_linear_forward(const void* x, const void* W, const void* bias, 
   p.clear_flags = clear_ahead ? 0 : 1;
   p.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + L.tickets);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.shares);
+  p.part_floats = static_cast<int64_t>(L.share_bytes / 4);
   const cudaError_t e = timed(kTLinear, s, [&] { return run_product(op, plan, x, W, M, d_out, d_in, p, dv.sms, s); });
   if (e != cudaSuccess) return cuda_fail(e, "linear launch");
   return ok();
@@ -522,6 +530,7 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
   p.flags = static_cast<uint32_t*>(workspace);
   p.tickets = reinterpret_cast<uint32_t*>(ws + L.tickets);
   p.part = reinterpret_cast<float*>(ws + L.shares);
+  p.part_floats = static_cast<int64_t>(L.share_bytes / 4);
   if (dx) {
     p.out = static_cast<uint16_t*>(dx);
     e = timed(kTLinearDx, s, [&] { return run_product(kLinDx, dx_plan, dz, W, M, d_in, d_out, p, dv.sms, s); });

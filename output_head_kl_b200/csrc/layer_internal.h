@@ -67,6 +67,7 @@ struct LinParams {
   int row_group;         //   row blocks swept together
   int splits;            // shares of the reduction (small tiles: the cluster size)
   float* part;           // large tiles: [shares][256 x bn] partial sums
+  int64_t part_floats;   //   room for them
   uint32_t* tickets;     //   [split tiles][16] arrivals, zero before the launch and after it
   const uint16_t* bias;      // [N] bf16 or null
   const uint16_t* residual;  // [M, N] bf16 or null
