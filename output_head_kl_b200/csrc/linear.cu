@@ -41,13 +41,37 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // bf16 rounding of the results; for z below -88 the exponential is inf and the result 0.
 __device__ __forceinline__ float sigmoid_f(float z) { return rcp_approx(1.0f + ex2_approx(-kLog2eL * z)); }
 
+// The normal distribution function Phi(z), and e = e^(-z^2 / 2), which the density needs too.  Its lower tail is
+// Phi(-a) = e^(-a^2 / 2) P(t) with t = 1 / (1 + p a), P a polynomial: the form of Hastings (Approximations for Digital
+// Computers, 1955), its coefficients a minimax fit to the scaled tail e^(a^2 / 2) Phi(-a) over 0 <= a <= 13.5, within
+// 1.6 x 2^-24 of it.  Nothing cancels for z << 0, where 1 + erf(z / sqrt 2) is 4 % off at z = -5; and the
+// exponential serves both.  Measured at 16384 x 1024 x 4096 with residual and z: 144 us, with erff 156, with erfcf
+// 208-221; the slopes' column sums there 81, 115 and 155 us.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float t = rcp_approx(fmaf(0.305f, fabsf(z), 1.0f));
+  float q = 0.0366991982f;
+  q = fmaf(q, t, -0.15298833f);
+  q = fmaf(q, t, 0.185716912f);
+  q = fmaf(q, t, -0.0379768386f);
+  q = fmaf(q, t, 0.121021681f);
+  q = fmaf(q, t, 0.103420869f);
+  q = fmaf(q, t, 0.122466817f);
+  q = fmaf(q, t, 0.121639736f);
+  e = ex2_approx(-0.5f * kLog2eL * z * z);
+  q = q * t * e;
+  return z < 0.f ? q : 1.0f - q;
+}
+
 // 2 u of the tanh form of GELU: 0.5 (1 + tanh u) = sigmoid(2 u).
 __device__ __forceinline__ float gelu_2u(float z) { return 1.5957691216057308f * fmaf(0.044715f * z * z, z, z); }
 
 template <int ACT>
 __device__ __forceinline__ float act_f(float z) {
   if (ACT == KDKL_ACT_RELU) return z < 0.f ? 0.f : z;   // NaN passes
-  if (ACT == KDKL_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (ACT == KDKL_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if (ACT == KDKL_ACT_GELU_TANH) return z * sigmoid_f(gelu_2u(z));
   if (ACT == KDKL_ACT_SILU) return z * sigmoid_f(z);
   return z;
@@ -57,8 +81,9 @@ template <int ACT>
 __device__ __forceinline__ float act_grad_f(float z) {
   if (ACT == KDKL_ACT_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);   // NaN passes
   if (ACT == KDKL_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
-    return fmaf(z * 0.3989422804014327f, ex2_approx(-0.5f * kLog2eL * z * z), cdf);
+    float e;
+    const float cdf = normal_cdf(z, e);
+    return fmaf(z * 0.3989422804014327f, e, cdf);
   }
   if (ACT == KDKL_ACT_GELU_TANH) {
     const float p = sigmoid_f(gelu_2u(z));
