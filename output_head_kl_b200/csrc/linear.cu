@@ -86,8 +86,11 @@ __device__ __forceinline__ float act_grad_f(float z) {
     return fmaf(z * 0.3989422804014327f, e, cdf);
   }
   if (ACT == KDKL_ACT_GELU_TANH) {
-    const float p = sigmoid_f(gelu_2u(z));
-    return fmaf(z * p * (1.0f - p), 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.0f), p);
+    // 2 u = z (k + k c z^2) and its slope k + 3 k c z^2, k = 2 sqrt(2 / pi), c = 0.044715; z^2 is held at 1e4, where
+    // p (1 - p) is 0 long since, so that it does not become inf
+    const float z2 = fminf(z * z, 1e4f);
+    const float p = sigmoid_f(z * fmaf(0.0713548163f, z2, 1.5957691216f));
+    return fmaf(z * p * (1.0f - p), fmaf(0.214064449f, z2, 1.5957691216f), p);
   }
   if (ACT == KDKL_ACT_SILU) {
     const float p = sigmoid_f(z);

@@ -18,6 +18,8 @@ U = 2.0 ** -24
 BF = torch.bfloat16
 D = 512
 TAIL = -torch.linspace(3.0, 11.0, D, dtype=torch.float64)
+HUGE = torch.tensor([s * v for v in (1e3, 1e5, 1e10, 1e18, 6e18, 1e19, 7e19, 1e20, 1e25, 1e30, 1e38, 3.3e38)
+                     for s in (1.0, -1.0)], dtype=torch.float64)
 
 
 def _cdf(z):
@@ -57,3 +59,25 @@ def test_gelu_slope_of_negative_values():
     z = TAIL.to(BF).double()
     a, b = _cdf(z), z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     assert bool(((_slopes(z, "gelu") - (a + b)).abs() <= (2 * z * z + 16) * U * (a.abs() + b.abs())).all())
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_slopes_of_huge_values(act):
+    """0 or 1 and never NaN, as far as bf16 reaches."""
+    z = HUGE.to(BF).double()
+    assert bool(torch.isfinite(z).all())
+    assert torch.equal(_slopes(z, act), (z > 0).double())
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+@pytest.mark.parametrize("rows,plan", [(1, 0), (300, 256)])
+def test_huge_values(act, rows, plan):
+    z = HUGE.to(BF).double()
+    y = _forward(z, act, rows, plan)
+    assert torch.equal(y, torch.where(z > 0, z, 0.0).expand_as(y))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_nan_passes(act):
+    z = torch.full((8,), float("nan"), dtype=torch.float64)
+    assert bool(torch.isnan(_slopes(z, act)).all()) and bool(torch.isnan(_forward(z, act, 1, 0)).all())
