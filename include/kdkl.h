@@ -345,9 +345,11 @@ typedef enum { KDKL_BF16 = 0, KDKL_F32 = 1, KDKL_E4M3 = 2 } kdkl_dtype;
  *               kdkl_rmsnorm_backward reads.  y is computed from the sum before it is rounded to h_dtype.
  *   y           [N, d] out, 16-byte aligned: KDKL_BF16 (the `hidden` of kdkl_forward), or KDKL_E4M3
  *   y_scale     [N] fp32 out, 4-byte aligned, for KDKL_E4M3 only (else NULL): the row's largest |y| / 448;
- *               the row's values are y_scale[n] * (e4m3 value).  A row of zeros has scale 0; a row with a
- *               NaN has scale NaN.
+ *               the row's values are y_scale[n] * (e4m3 value).  A row with a NaN has scale NaN.
  *   N >= 0, d % 8 == 0, 8 <= d <= 32768, eps finite and >= 0
+ * A row of zeros has y = 0 and scale 0, with eps = 0 too.  The sum of squares is held in fp32: a finite row whose
+ * squares sum to more than 3.4e38 has y = 0 and scale 0, and where eps is 0, so that nothing stands beside them,
+ * squares below 1e-38 lose bits; a row whose squares all vanish (|h| below about 1e-23) counts as a row of zeros.
  * h may be residual itself or, where the types agree, x; y may be x where both are bf16 and h is another
  * buffer.  No workspace.  N = 0 writes nothing.
  */
@@ -366,7 +368,8 @@ kdkl_status kdkl_rmsnorm_forward(const void* x, const void* residual, const void
  *   dx      [N, d] out of h_dtype, 16-byte aligned: the gradient of x and of residual alike; may be dh
  *   dgamma  [d] fp32 out, 4-byte aligned, overwritten
  *   workspace >= kdkl_rmsnorm_workspace_bytes(N, d), 256-byte aligned (it holds no device flags)
- * An e4m3 y has the same gradient: rounding is passed through.  N = 0 writes dgamma = 0.
+ * An e4m3 y has the same gradient: rounding is passed through.  A row that counts as zeros with eps = 0 (see the
+ * forward) has dx = dh and adds nothing to dgamma.  N = 0 writes dgamma = 0.
  */
 size_t kdkl_rmsnorm_workspace_bytes(int64_t N, int32_t d);
 kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gamma, const void* dh, int64_t N,
