@@ -83,7 +83,8 @@ enum {
                               so this call's outputs, and those of every later call on the stream
                               that read them, are invalid */
   KDKL_DEV_BOUNDS = 16u    /* bounds-checking build (libkdkl_debug.so) only: an index check in a
-                              kernel failed and the access was skipped; outputs are invalid */
+                              kernel failed and the access was skipped; outputs are invalid
+                              (the RMS norm's kernels have no flag word and no such checks) */
 };
 
 /*

@@ -5,10 +5,12 @@ Every kernel is compiled for sm_100a only.  Run ``python -m output_head_kl_b200.
 
 A second library, ``_lib/libkdkl_debug.so``, is the same sources compiled with
 ``-DKDKL_DEBUG``: every list walk, partial-result slot, shared-memory list write,
-TMA coordinate and lockstep slot is range-checked in the kernels, and a failed
-check sets ``KDKL_DEV_BOUNDS`` in the device flag word and skips (or clamps) the
-access instead of making it.  It stands in for a memory checker, which this
-hardware pool does not offer; the tests run the ragged parity cases through it.
+TMA coordinate and lockstep slot of the loss and top-K kernels is range-checked, and
+so are the linear layer's partial sums and tickets in the workspace, its direct loads
+and stores and its TMA stores; a failed check sets ``KDKL_DEV_BOUNDS`` in the device
+flag word and skips (or clamps) the access instead of making it.  It stands in for a
+memory checker; the tests run the ragged parity cases through it.  The RMS norm has
+no flag word and no such checks.
 
 A third, ``_lib/libkdkl_prof.so``, is compiled with ``-DKDKL_PROFILE``: the same
 kernels, which also count the SM cycles their TMA producer, MMA issuer and

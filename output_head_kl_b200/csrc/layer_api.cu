@@ -15,11 +15,8 @@ namespace {
 
 constexpr int32_t kMaxWidth = 1 << 20;
 constexpr size_t kFlagBytes = 256;
-// Shares of split tiles that a launch of large tiles may have (a wave of CTA pairs has 74 on B200; each leaves
-// 256 x bn fp32 partial sums), and the tickets of their tiles.
-constexpr int kMaxShares = 80;
 constexpr int kMaxTailSplits = 8;
-constexpr size_t kTicketBytes = kMaxShares / 2 * kTileTickets * 4;
+constexpr size_t kTicketBytes = kMaxSplitTiles * kTileTickets * 4;
 
 bool float_dtype(int32_t t) { return t == KDKL_BF16 || t == KDKL_F32; }
 
@@ -520,7 +517,8 @@ kdkl_status kdkl_linear_backward(const void* dy, const void* pre, const void* x,
     e = timed(kTActGrad, s, [&] {
       return launch_act_grad(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(pre), o.activation, M,
                              d_out, dz_out, reinterpret_cast<float*>(ws + L.part),
-                             reinterpret_cast<uint32_t*>(ws + L.col_tickets), dbias,
+                             static_cast<int64_t>((L.total - L.part) / 4),
+                             reinterpret_cast<uint32_t*>(ws + L.col_tickets), dbias, reinterpret_cast<uint32_t*>(ws),
                              act_grad_chunks(M, d_out, dv.sms), s);
     });
     if (e != cudaSuccess) return cuda_fail(e, "activation gradient launch");

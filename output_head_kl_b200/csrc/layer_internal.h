@@ -81,6 +81,10 @@ struct LinParams {
 };
 
 constexpr int kTileTickets = 16;   // epilogue warps of a CTA pair
+// Shares of split tiles that a launch of large tiles may have (a wave of CTA pairs has 74 on B200; each leaves
+// 256 x bn fp32 partial sums), and the tiles that have two at least.
+constexpr int kMaxShares = 80;
+constexpr int kMaxSplitTiles = kMaxShares / 2;
 // Large tiles: 256 x bn (bn = 256, 192 or 128) by CTA pairs, persistent.
 struct PairMaps {
   CUtensorMap a, b;           // operands
@@ -95,12 +99,14 @@ cudaError_t launch_linear_small(int op, int nt, const CUtensorMap& tmA, const CU
                                 cudaStream_t s);
 
 // dz = dy * act'(pre) in bf16 (dz may be null: column sums only, of dy when act is none) and, with dbias, the
-// column sums of its fp32 values, by way of part[chunks, n] and one ticket per 256 columns (zero before).
+// column sums of its fp32 values, by way of part[chunks, n] and one ticket per 256 columns (zero before).  flags is
+// written by the bounds-checking build only.
 constexpr int kMaxSms = 512;         // workspaces are sized for any device up to this many SMs
 constexpr int kMaxActChunks = 256;   // row ranges that the last block of a column range adds up
 int act_grad_chunks(int64_t M, int n, int sms);
 cudaError_t launch_act_grad(const uint16_t* dy, const uint16_t* pre, int act, int64_t M, int n, uint16_t* dz,
-                            float* part, uint32_t* tickets, float* dbias, int chunks, cudaStream_t s);
+                            float* part, int64_t part_floats, uint32_t* tickets, float* dbias, uint32_t* flags,
+                            int chunks, cudaStream_t s);
 
 // Launch configuration of these kernels: all of them wait for the kernels before them by themselves
 // (pdl_wait), so that their set-up overlaps the end of the one before.

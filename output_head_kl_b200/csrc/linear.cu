@@ -273,6 +273,7 @@ struct Finisher {
 
   // bias and scales of columns [col, col + 4) at offset `at` of the warp's columns
   __device__ __forceinline__ void load_side(int col, int at) const {
+    if (!dbg_ok(col >= 0 && col + 4 <= p.N, p.flags)) return;
     if (p.bias) {
       const uint2 b = *reinterpret_cast<const uint2*>(p.bias + col);
       st_shared_v4(bias + at * 4, __float_as_uint(bf_lo(b.x)), __float_as_uint(bf_hi(b.x)),
@@ -628,8 +629,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       float4* mine = reinterpret_cast<float4*>(
           p.part + (static_cast<int64_t>(w.share) * (2 * kEpiWarps) + wslot) * warp_floats);
       if (split) {
+        // the last share of this tile, and the tile's ticket, lie in their parts of the workspace
+        const int tile0 = w.share / p.splits;
+        const bool room = dbg_ok(static_cast<int64_t>(tile0 + 1) * p.splits * (2 * kEpiWarps) * warp_floats <=
+                                         p.part_floats && tile0 < kMaxSplitTiles, p.flags);
 #pragma unroll 1
-        for (int c = 0; c < BN / 64; ++c) {
+        for (int c = 0; c < BN / 64 && room; ++c) {
           if (c_first + c * 32 >= p.N) break;
           float v[32];
           tmem_ld32(tbase + c * 32, v);
@@ -639,9 +644,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __stcg(mine + (c * 8 + g) * 32 + lane, make_float4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]));
         }
         release_acc();
+        if (!room) continue;
         __threadfence();
         __syncwarp();
-        uint32_t* ticket = p.tickets + w.share / p.splits * (2 * kEpiWarps) + wslot;
+        uint32_t* ticket = p.tickets + tile0 * (2 * kEpiWarps) + wslot;
         int last = 0;
         if (lane == 0) {
           last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(p.splits - 1);
@@ -1025,7 +1031,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
     d.res = d.bias = make_uint2(0u, 0u);
     d.xs = 1.f;
-    if (!L::kFull || i >= i1 || col >= p.N) return;
+    if (!L::kFull || i >= i1 || col >= p.N || !dbg_ok(row < p.M && col + 4 <= p.N, p.flags)) return;
     if (p.residual) d.res = *reinterpret_cast<const uint2*>(p.residual + static_cast<int64_t>(row) * p.N + col);
     if (p.bias) d.bias = *reinterpret_cast<const uint2*>(p.bias + col);
     if (L::kF8) {
@@ -1125,7 +1131,7 @@ __global__ void __launch_bounds__(kSmallThreads)
       for (int b = 0; b < kBatch; ++b) {
         const int i = first + b * kSmallThreads;
         const int row = row0 + (i >> 5), col = col0 + (i & 31) * 4;
-        if (i >= i1 || col >= p.N) continue;
+        if (i >= i1 || col >= p.N || !dbg_ok(row < p.M && col + 4 <= p.N, p.flags)) continue;
         const int64_t at = static_cast<int64_t>(row) * p.N + col;
         float v[4] = {q[b][0].x, q[b][0].y, q[b][0].z, q[b][0].w};
 #pragma unroll
@@ -1171,8 +1177,8 @@ constexpr int kActRows = 8;
 template <int ACT>
 __global__ void __launch_bounds__(32 * kActRows)
     act_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ pre, int64_t M, int n,
-                    uint16_t* __restrict__ dz, float* __restrict__ part, uint32_t* __restrict__ tickets,
-                    float* __restrict__ dbias) {
+                    uint16_t* __restrict__ dz, float* __restrict__ part, int64_t part_floats,
+                    uint32_t* __restrict__ tickets, float* __restrict__ dbias, uint32_t* __restrict__ flags) {
   __shared__ float s[kActRows][32][9];
   __shared__ int s_last;
   pdl_wait();
@@ -1191,6 +1197,7 @@ __global__ void __launch_bounds__(32 * kActRows)
       for (int u = 0; u < kU; ++u) {
         const int64_t at = (r + u * kActRows) * n + col;
         if (r + u * kActRows < r1) {
+          if (!dbg_ok(r1 <= M && at >= 0 && col + 8 <= n, flags)) return;
           g[u] = ld_stream16(dy + at);
           if (ACT != KDKL_ACT_NONE) z[u] = ld_stream16(pre + at);
         }
@@ -1227,6 +1234,7 @@ __global__ void __launch_bounds__(32 * kActRows)
     for (int r = 0; r < kActRows; ++r) t += s[r][c >> 3][c & 7];
     return t;
   };
+  if (!dbg_ok(static_cast<int64_t>(gridDim.y) * n <= part_floats, flags)) return;
   if (out < n) part[static_cast<int64_t>(blockIdx.y) * n + out] = column();
   // The block that finishes these columns last adds up the partial sums of all row ranges, in their order:
   // the result does not depend on which block that is.
@@ -1368,19 +1376,18 @@ int act_grad_chunks(int64_t M, int n, int sms) {
 }
 
 cudaError_t launch_act_grad(const uint16_t* dy, const uint16_t* pre, int act, int64_t M, int n, uint16_t* dz,
-                            float* part, uint32_t* tickets, float* dbias, int chunks, cudaStream_t s) {
-  LaunchConfig cfg(dim3((n + 255) / 256, chunks), dim3(32, kActRows), 0, 0, s);
+                            float* part, int64_t part_floats, uint32_t* tickets, float* dbias, uint32_t* flags,
+                            int chunks, cudaStream_t s) {
+  const LaunchConfig cfg(dim3((n + 255) / 256, chunks), dim3(32, kActRows), 0, 0, s);
+  const auto launch = [&](auto* kernel) {
+    return cudaLaunchKernelEx(&cfg.c, kernel, dy, pre, M, n, dz, part, part_floats, tickets, dbias, flags);
+  };
   switch (act) {
-    case KDKL_ACT_NONE:
-      return cudaLaunchKernelEx(&cfg.c, act_grad_kernel<KDKL_ACT_NONE>, dy, pre, M, n, dz, part, tickets, dbias);
-    case KDKL_ACT_RELU:
-      return cudaLaunchKernelEx(&cfg.c, act_grad_kernel<KDKL_ACT_RELU>, dy, pre, M, n, dz, part, tickets, dbias);
-    case KDKL_ACT_GELU:
-      return cudaLaunchKernelEx(&cfg.c, act_grad_kernel<KDKL_ACT_GELU>, dy, pre, M, n, dz, part, tickets, dbias);
-    case KDKL_ACT_GELU_TANH:
-      return cudaLaunchKernelEx(&cfg.c, act_grad_kernel<KDKL_ACT_GELU_TANH>, dy, pre, M, n, dz, part, tickets, dbias);
-    case KDKL_ACT_SILU:
-      return cudaLaunchKernelEx(&cfg.c, act_grad_kernel<KDKL_ACT_SILU>, dy, pre, M, n, dz, part, tickets, dbias);
+    case KDKL_ACT_NONE: return launch(act_grad_kernel<KDKL_ACT_NONE>);
+    case KDKL_ACT_RELU: return launch(act_grad_kernel<KDKL_ACT_RELU>);
+    case KDKL_ACT_GELU: return launch(act_grad_kernel<KDKL_ACT_GELU>);
+    case KDKL_ACT_GELU_TANH: return launch(act_grad_kernel<KDKL_ACT_GELU_TANH>);
+    case KDKL_ACT_SILU: return launch(act_grad_kernel<KDKL_ACT_SILU>);
     default: return cudaErrorInvalidValue;
   }
 }

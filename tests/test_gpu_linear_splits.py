@@ -32,3 +32,23 @@ def test_weight_gradient_of_many_shares(M, d_in, d_out, plan):
     both = TL._grad(*args, "silu", dw_plan=plan)
     alone = TL._grad(*args, "silu", dw_plan=plan, want=("dW",))
     assert torch.equal(both[1], alone[1])      # dx, which uses the same workspace first, changes nothing
+
+
+@pytest.fixture
+def debug_lib(monkeypatch):
+    monkeypatch.setattr(K, "_lib", None)
+    monkeypatch.setattr(K, "LIB_PATH", K.DEBUG_LIB_PATH)
+    yield
+    monkeypatch.setattr(K, "_lib", None)
+
+
+def test_bounds_checking_build(debug_lib):
+    """The same plans, every kind of forward tile and the column sums through the library that checks shares,
+    tickets, direct loads and stores: the results hold, and no check fails (TL._check and _check_grad read the flags)."""
+    assert K.lib()._name == K.DEBUG_LIB_PATH
+    for M, d_in, d_out, plan in CASES:
+        TL._check_grad(*TL._grad_data(M, d_in, d_out, seed=32), "gelu", dw_plan=plan)
+    for f8 in (False, True):
+        for plan in (1016, 2064, 8128, 128, 20192, 40256):
+            TL._check(TL._data(130, 2048, 136, f8, seed=33), "gelu", pre=True, plan=plan)
+    TL._check(TL._data(5000, 576, 2088, seed=34), "silu", pre=True, plan=20256, rows=slice(4700, 5000))
