@@ -400,9 +400,18 @@ def _fast():
     if _binding is None:
         import importlib.machinery
         import importlib.util
-        _import_torch()
+        torch = _import_torch()
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"kdkl binding not built: {BINDING_PATH} is missing "
+                               "(run `python -m output_head_kl_b200.build`)")
+        # it is compiled against torch's C++ headers: another torch needs another build
+        try:
+            with open(BINDING_PATH + ".torch") as f:
+                built = f.read()
+        except OSError:
+            built = "an unknown version"
+        if built != torch.__version__:
+            raise RuntimeError(f"kdkl binding built against torch {built}, torch {torch.__version__} is installed "
                                "(run `python -m output_head_kl_b200.build`)")
         loader = importlib.machinery.ExtensionFileLoader("kdkl_binding", BINDING_PATH)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("kdkl_binding", loader))

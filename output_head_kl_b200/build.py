@@ -97,12 +97,28 @@ def _build_binding():
     os.replace(BINDING + ".tmp", BINDING)
 
 
+def _torch_with_cuda() -> str | None:
+    """The installed torch's version; None without torch, or with one built without CUDA."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__ if torch.version.cuda else None
+
+
+def _binding_stale(torch_version: str) -> bool:
+    """Also when the binding was built against another torch."""
+    try:
+        with open(BINDING + ".torch") as f:
+            return f.read() != torch_version or _stale(BINDING)
+    except OSError:
+        return True
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True, profile: bool = True) -> str:
-    """Builds libkdkl.so and its binding (and, when asked, the bounds-checking libkdkl_debug.so and the
-    cycle-counting libkdkl_prof.so)."""
+    """Builds libkdkl.so (and, when asked, the bounds-checking libkdkl_debug.so and the cycle-counting
+    libkdkl_prof.so), which need nvcc alone, then the Python binding's compiled part, which needs torch."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    if force or _stale(BINDING):
-        _build_binding()
     if force or _stale(LIB):
         logs = _build_one(LIB, "", [], "ptxas.log")
         if verbose:
@@ -111,6 +127,13 @@ def build(force: bool = False, verbose: bool = False, debug: bool = True, profil
         _build_one(DEBUG_LIB, "dbg_", ["-DKDKL_DEBUG"], "ptxas_debug.log")
     if profile and (force or _stale(PROFILE_LIB)):
         _build_one(PROFILE_LIB, "prof_", ["-DKDKL_PROFILE"], "ptxas_prof.log")
+    torch_version = _torch_with_cuda()
+    if torch_version is None:
+        print("kdkl: no torch with CUDA, the Python binding is not built (the C library is)", file=sys.stderr)
+    elif force or _binding_stale(torch_version):
+        _build_binding()
+        with open(BINDING + ".torch", "w") as f:
+            f.write(torch_version)
     return LIB
 
 
