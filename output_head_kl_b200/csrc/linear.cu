@@ -357,8 +357,8 @@ struct Finisher {
 //
 // Bound by the tensor cores and, equally, by what an SM takes in from L2: a 64-wide reduction block of a 256 x 256
 // tile is 512 cycles of MMA and 32 KB a CTA, 64 bytes a cycle.  Measured at 16384 x 4096 x 4096 under the power cap:
-// plain product 403-415 us (cuBLAS 402-405), with SiLU, residual and z stored 461-473; dx 409, dW 433 (the last
-// wave split: 459 without).  An epilogue of one tile takes 4,000 (plain) to 10,700 cycles (everything).
+// plain product 404 us (cuBLAS 401), with bias, SiLU, residual and z stored 458-465; dx 408, dW 429 (the last
+// wave split: 448 without).  An epilogue of one tile takes 4,000 (plain) to 10,700 cycles (everything).
 // ============================================================================
 constexpr int kPairThreads = 320;
 constexpr int kEpiWarps = 8;
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ([32-column chunk][4 columns][row], so that both ways move consecutive 16-byte groups), and after a cluster
 // barrier each CTA joins and finishes BN / splits columns of its 128 rows, adding the shares in pair order.
 // The epilogue is shared out with the join, so splitting costs no more than it saves there: 512 x 4096 x 4096 in
-// 19.9 us against 26.4 us unsplit.
+// 17.7 us against 23.8 us unsplit, with bias, SiLU, residual and z in 19.6 against 29.0.
 // ============================================================================
 template <int OP, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -927,8 +927,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // share of the reduction blocks into a [128 x NT] TMEM tile, spills it to shared memory as [row][column]
 // fp32, and after a cluster barrier each CTA joins and finishes 1 / splits of the tile: for every output it
 // adds the partial sums in CTA order.  No workspace, no atomics, one launch.  Bound by HBM while the weights stream
-// (1 x 4096 x 4096: 9,300 of 16,600 cycles), else by set-up, the first bytes' latency and the join; 10.2 us back to
-// back, e4m3 7.2 us.
+// (1 x 4096 x 4096: 9,300 of 16,600 cycles), else by set-up, the first bytes' latency and the join; back to back
+// with the weights from HBM 8.9 us (from L2 7.2), 8 rows in e4m3 6.6 us (6.0).
 // ============================================================================
 constexpr int kSmallThreads = 192;
 constexpr int kMaxSplits = 8;
@@ -1169,8 +1169,9 @@ __global__ void __launch_bounds__(kSmallThreads)
 // ============================================================================
 // dz = dy act'(pre), bf16, and the column sums of its fp32 values
 //
-// One block: 256 columns (8 per thread) x a range of rows, eight rows at a time.  Bound by HBM: 67 us for
-// 16384 x 4096 with SiLU, 6.0 TB/s.
+// One block: 256 columns (8 per thread) x a range of rows, eight rows at a time.  Bound by HBM where dz is
+// written: 16384 x 4096 with SiLU in 65 us, 6.2 TB/s, with the column sums 70 us; the column sums alone, which write
+// nothing, by the slopes' arithmetic: 56 us, 4.8 TB/s (GELU 67 us).
 // ============================================================================
 constexpr int kActRows = 8;
 

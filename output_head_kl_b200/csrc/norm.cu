@@ -139,7 +139,8 @@ __device__ __forceinline__ void row_reduce(float& sum, float& top, float2* slots
 // One row per warp (WARP: four rows a block, d <= 256 VPT) or per block.  A thread holds VPT steps of
 // kV elements.  Nothing is kept between rows, so the grid is one block per row (or four rows): the
 // next block's loads cover this one's barrier.  Measured (x and y bf16): 32768 x 4096 in 156 us, 6.9 TB/s;
-// 65536 x 1024 in 81 us, 6.6 TB/s; e4m3 output 139 us, 6.8 TB/s; one row of 4096 in 1.8 us.
+// 65536 x 1024 in 80 us, 6.7 TB/s; e4m3 output 140 us, 6.7 TB/s; one row of 4096 in 1.9 us.  Rows above 16384
+// elements (eight steps) spill up to 188 bytes a thread: 4096 x 32768 in 191 us, 5.6 TB/s.
 template <bool XF32, bool HF32, bool Q, int VPT, bool WARP>
 __global__ void __launch_bounds__(kNormMaxThreads) rmsnorm_kernel(const NormParams p) {
   __shared__ float2 s_red[32];
@@ -260,11 +261,14 @@ __device__ __forceinline__ void cp_async_wait() {
 // A block's rows follow one another, so the next rows' loads have to be in flight while this one is
 // reduced: each thread copies its own 16-byte pieces of the next kGradStages - 1 rows to shared memory
 // asynchronously (it alone reads them, so no barrier is needed), which costs no registers.  Measured (bf16):
-// 32768 x 4096 in 161 us with launch_colsum, 6.7 TB/s (183 us with plain loads, 241 us with the next row in
-// registers, which halves the resident blocks); 1003 x 896 with an fp32 stream in 10.6 us.
+// 32768 x 4096 in 170 us with launch_colsum, 6.3 TB/s (where the ways to load were compared it took 161 us, against
+// 183 with plain loads and 241 with the next row in registers, which halves the resident blocks); 1003 x 896 with an
+// fp32 stream in 9.9 us.
 constexpr int grad_pieces(int vpt, bool h_f32) { return vpt * (1 + 2 * (h_f32 ? 2 : 1)); }
 constexpr int kGradStages = 3;
-// Rows beyond 16 elements a thread do not fit the ring: they are read twice, the second time from L2.
+// Rows beyond 16 elements a thread do not fit the ring: they are read twice, the second time from L2, with nothing in
+// flight across the barrier (fp32, 16384 x 8192: 409 us, 4.6 TB/s; bf16, 8192 x 16384: 353 us, 3.0 TB/s, and 16384 x
+// 8200, one block an SM: 624 us, 1.7 TB/s).
 constexpr bool grad_ring(int vpt) { return vpt <= 2; }
 
 template <bool HF32, int VPT, bool WARP>
