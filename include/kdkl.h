@@ -328,7 +328,8 @@ kdkl_status kdkl_teacher_topk(const void* hidden, const void* W, int64_t N, int3
  * Same conventions as above: dense row-major tensors of the current device,
  * caller-owned workspaces, asynchronous on `stream`, host checks before any
  * launch, results that repeat bit for bit; every call can be captured in a CUDA
- * graph after one eager call.  Tensors without rows (N or M = 0) may be NULL.  Every row takes part: rows of padding hold finite
+ * graph after one eager call.  Calls that may overlap (on other streams, or in graphs replayed at once) need workspaces of
+ * their own.  Tensors without rows (N or M = 0) may be NULL.  Every row takes part: rows of padding hold finite
  * values (a NaN or infinity in a row spreads to that row's outputs, and in a
  * gradient to the column sums and weight gradients that the row enters).
  * ---------------------------------------------------------------------------
@@ -393,8 +394,7 @@ kdkl_status kdkl_rmsnorm_backward(const void* dy, const void* h, const void* gam
  *   M >= 0, d_out % 8 == 0, d_in, d_out <= 2^20
  *   options   NULL = bf16 operands, no activation, the planner's tiles
  *   workspace >= kdkl_linear_workspace_bytes(M, d_in, d_out, 0), 256-byte aligned; it holds the device flag
- *             word (kdkl_read_device_flags) and no other state.  Calls that may overlap need workspaces of
- *             their own.
+ *             word (kdkl_read_device_flags) and no other state
  * Products are summed in fp32.  M = 0 writes nothing.
  *
  * Activations: KDKL_ACT_GELU is z Phi(z) (the error-function form), KDKL_ACT_GELU_TANH its tanh approximation,
